@@ -336,6 +336,134 @@ muon_status_t muon_check_bounded_wait(void* workspace, int64_t limit_us, void* s
  * MUON_STEP_SKIPPED). */
 muon_status_t muon_query_status(void* workspace, void* stream);
 
+/* ---- Operators around the step (no counterpart on the pages) -------------
+ *
+ * The calls that read the weights this library steps and make their
+ * gradients: the embedding, the language-model head's loss, and the experts'
+ * products.  They follow the rules above (ownership, device checks, stream
+ * order, errors).  Matrices are row-major; `*_ld` is the distance between
+ * consecutive rows in elements (>= the row length).  Element types are
+ * muon_dtype_t; index arrays are int32 or int64 (muon_index_t).  Buffers must
+ * be aligned to their element; rows and bases that are multiples of 16 bytes
+ * avoid a copy into the workspace.  Buffers that a call writes must not
+ * overlap any other buffer of the call, nor a row another row of the same
+ * buffer.  A workspace is device memory, 256-byte aligned, not used by other
+ * work until the call has finished on `stream`; its contents are scratch but
+ * for the status word that muon_query_status reads: 0, MUON_ERR_TIMEOUT, or
+ * MUON_ERR_INVALID_ARG when an index array held a value the call had to leave
+ * out (see each call).  Every result is the same, bit for bit, from call to
+ * call on the same inputs.  The calls enqueue kernels only, so they may be
+ * captured into a graph once one call has run on the device outside a
+ * capture. */
+typedef enum { MUON_I32 = 0, MUON_I64 = 1 } muon_index_t;
+
+/* out[t] = scale * table[ids[t]], t < tokens: one product in fp32, rounded
+ * once to out_dtype.  Rows whose id is `padding_idx` or lies outside
+ * [0, vocab) are written as zeros (pass padding_idx -1 for none).
+ * table: vocab x dim; out: tokens x dim.  tokens == 0 is a no-op. */
+muon_status_t muon_embedding_lookup(const void* table, int32_t table_dtype, int64_t table_ld,
+                                    int64_t vocab, int64_t dim, const void* ids,
+                                    int32_t ids_dtype, int64_t tokens, float scale,
+                                    int64_t padding_idx, void* out, int32_t out_dtype,
+                                    int64_t out_ld, void* stream);
+
+/* Workspace bytes of muon_embedding_grad (0 on bad sizes). */
+size_t muon_embedding_grad_workspace(int64_t tokens, int64_t vocab, int64_t dim);
+
+/* The lookup's gradient: d_table[v] = scale * sum of grad[t] over the tokens
+ * with ids[t] == v, in token order within fixed pieces, in fp32.
+ * d_table: fp32, vocab x dim, contiguous (the form adamw_step takes); with
+ * accumulate == 0 every row is written (zeros for a row without tokens),
+ * with accumulate == 1 the sums are added to it and rows without tokens are
+ * left alone.  Tokens whose id is `padding_idx` are left out unread, and so
+ * are those outside [0, vocab), which also set the status
+ * MUON_ERR_INVALID_ARG.  tokens, vocab < 2^31. */
+muon_status_t muon_embedding_grad(const void* grad, int32_t grad_dtype, int64_t grad_ld,
+                                  const void* ids, int32_t ids_dtype, int64_t tokens,
+                                  int64_t vocab, int64_t dim, float scale, int64_t padding_idx,
+                                  int32_t accumulate, float* d_table, void* workspace,
+                                  size_t ws_bytes, void* stream);
+
+/* Softmax cross entropy of a linear head, z = logit_scale * hidden weight^T
+ * (tokens x vocab, never held for more than a block of tokens):
+ *   lse[t]  = ln sum_v exp(z[t][v])
+ *   loss[t] = lse[t] - z[t][targets[t]]; 0 for ignored tokens
+ * A token is ignored when its target is `ignore_index` or lies outside
+ * [0, vocab); the latter also sets the status MUON_ERR_INVALID_ARG.
+ * hidden (tokens x dim) and weight (vocab x dim) are both MUON_BF16 or both
+ * MUON_F16.  The fields from row_scale on are read by muon_linear_ce_grad. */
+typedef struct {
+    const void* hidden;
+    const void* weight;
+    const void* targets;
+    float* loss;            /* tokens, fp32                                   */
+    float* lse;             /* tokens, fp32                                   */
+    int64_t tokens, vocab, dim;
+    int64_t hidden_ld, weight_ld;
+    int64_t ignore_index;
+    int32_t dtype;          /* of hidden and weight                           */
+    int32_t targets_dtype;  /* muon_index_t                                   */
+    float logit_scale;
+    int32_t d_weight_dtype; /* dtype, or MUON_F32                             */
+    const float* row_scale; /* tokens, fp32: d objective / d loss[t]; NULL: 1 */
+    void* d_hidden;         /* tokens x dim, dtype, contiguous                */
+    void* d_weight;         /* vocab x dim, contiguous                        */
+    int32_t accumulate;     /* 1: d_weight += (MUON_F32 only)                 */
+    int32_t reserved;       /* must be 0                                      */
+} muon_linear_ce_t;
+
+/* Workspace bytes for muon_linear_ce (with_grad 0) or muon_linear_ce_grad
+ * (1): for one block of all tokens when that fits in `budget_bytes`, else the
+ * most that blocks of a multiple of 256 tokens can use of it, or what 256
+ * tokens need when that is more.  Reads the sizes, dtypes, strides and
+ * pointers' alignment only.  0 on bad sizes. */
+size_t muon_linear_ce_workspace(const muon_linear_ce_t* p, int32_t with_grad, size_t budget_bytes);
+
+/* loss and lse alone. */
+muon_status_t muon_linear_ce(const muon_linear_ce_t* p, void* workspace, size_t ws_bytes,
+                             void* stream);
+
+/* loss, lse and both gradients of sum_t row_scale[t] * loss[t]:
+ *   g[t][v]  = row_scale[t] (exp(z - lse) - [v == targets[t]]), 0 when ignored
+ *   d_hidden = logit_scale g weight;  d_weight = logit_scale g^T hidden
+ * g is rounded once to `dtype`, relative to the largest |row_scale|; the sums
+ * are fp32.  Ignored tokens' hidden rows do not enter d_weight, whatever
+ * they hold. */
+muon_status_t muon_linear_ce_grad(const muon_linear_ce_t* p, void* workspace, size_t ws_bytes,
+                                  void* stream);
+
+/* Products grouped by expert.  The tokens' rows are sorted by expert: expert
+ * e has rows [offsets[e], offsets[e+1]), offsets (device, experts + 1
+ * entries) nondecreasing in [0, tokens]; any expert may have none.  A value
+ * outside is moved to the nearest end, and a range that runs backwards is
+ * empty.  dtype is MUON_BF16 or MUON_F16 for rows and weights.
+ *
+ * transpose == 0: y[t] = weight[e] x[t]    x: tokens x cols, y: tokens x rows
+ * transpose == 1: y[t] = weight[e]^T x[t]  x: tokens x rows, y: tokens x cols
+ * (the second is the first's input gradient).  weight: experts x rows x
+ * cols, contiguous.  Rows of y that belong to no expert are zeros.  fp32
+ * sums, rounded once to y's type, which is dtype. */
+size_t muon_expert_matmul_workspace(const void* x, int64_t x_ld, const void* weight,
+                                    int64_t experts, int64_t tokens, int64_t rows, int64_t cols,
+                                    int32_t transpose);
+muon_status_t muon_expert_matmul(const void* x, int64_t x_ld, const void* weight,
+                                 const void* offsets, int32_t offsets_dtype, int32_t dtype,
+                                 int64_t experts, int64_t tokens, int64_t rows, int64_t cols,
+                                 int32_t transpose, void* y, int64_t y_ld, void* workspace,
+                                 size_t ws_bytes, void* stream);
+
+/* The weights' gradient: d_weight[e] = sum over expert e's rows t of
+ * grad[t] x[t]^T (experts x rows x cols, contiguous; zeros for an expert
+ * without rows).  grad: tokens x rows; x: tokens x cols.  d_weight_dtype:
+ * dtype or MUON_F32; accumulate == 1 adds to it (MUON_F32 only). */
+size_t muon_expert_wgrad_workspace(const void* grad, int64_t grad_ld, const void* x, int64_t x_ld,
+                                   int64_t experts, int64_t tokens, int64_t rows, int64_t cols);
+muon_status_t muon_expert_wgrad(const void* grad, int64_t grad_ld, const void* x, int64_t x_ld,
+                                const void* offsets, int32_t offsets_dtype, int32_t dtype,
+                                int64_t experts, int64_t tokens, int64_t rows, int64_t cols,
+                                void* d_weight, int32_t d_weight_dtype, int32_t accumulate,
+                                void* workspace, size_t ws_bytes, void* stream);
+
 /* ---- Instrumentation (no counterpart on the pages) --------------------- */
 
 /* Kernel kinds the library launches. */
@@ -351,7 +479,15 @@ typedef enum {
     MUON_KERNEL_GRAD_GUARD = 8,     /* global gradient norm / non-finite    */
     MUON_KERNEL_DESC_UPLOAD = 9,    /* per-matrix records into the workspace */
     MUON_KERNEL_STATS = 10,         /* per-matrix step statistics           */
-    MUON_KERNEL_COUNT = 11
+    MUON_KERNEL_EMBED_LOOKUP = 11,  /* embedding rows                       */
+    MUON_KERNEL_EMBED_SORT = 12,    /* token positions sorted by id         */
+    MUON_KERNEL_EMBED_GRAD = 13,    /* embedding gradient sums              */
+    MUON_KERNEL_CE_LOGITS = 14,     /* head logits and their softmax sums   */
+    MUON_KERNEL_CE_ROWS = 15,       /* per-token loss and logit gradients   */
+    MUON_KERNEL_CE_GRAD = 16,       /* head gradient products               */
+    MUON_KERNEL_EXPERT = 17,        /* expert products                      */
+    MUON_KERNEL_PACK = 18,          /* rows copied to a 16-byte pitch       */
+    MUON_KERNEL_COUNT = 19
 } muon_kernel_kind_t;
 
 /* Process-wide count of kernels this library has launched (all kinds); a

@@ -17,6 +17,11 @@ Functions keep the C names:
     muon_query_status(workspace, stream=None)
     MuonAdamW(muon_params, adamw_params, muon_hp, adamw_hp): a torch.optim.Optimizer
     muon_step_graph_create / _launch / _destroy (through MuonBatch.capture)
+and, in train.py, the operators that read the stepped weights and make their
+gradients:
+    muon_embedding_lookup, muon_embedding_grad
+    muon_linear_ce, muon_linear_ce_grad
+    muon_expert_matmul, muon_expert_wgrad
 """
 from __future__ import annotations
 
@@ -27,6 +32,10 @@ from dataclasses import dataclass
 from typing import Optional, Sequence
 
 import numpy as np
+
+from . import train
+from .train import (muon_embedding_grad, muon_embedding_lookup, muon_expert_matmul, muon_expert_wgrad,
+                    muon_linear_ce, muon_linear_ce_grad, muon_linear_ce_workspace)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmuonstep.so")
@@ -45,9 +54,11 @@ EXPORTS = ("muon_workspace_bytes_per_matrix", "muon_workspace_size", "muon_plan"
            "muon_status_string", "muon_version", "muon_launch_count", "muon_set_timing",
            "muon_timing_read", "muon_kernel_name", "muon_step_batched_noalloc",
            "muon_check_bounded_wait", "muon_step_graph_create", "muon_step_graph_launch",
-           "muon_step_graph_destroy", "muon_step_batched_stats", "adamw_step_batched")
+           "muon_step_graph_destroy", "muon_step_batched_stats", "adamw_step_batched",
+           *train.EXPORTS)
 KERNEL_KINDS = ("momentum_norm", "norm_finalize", "x0_rescale", "ns_syrk", "ns_poly",
-                "ns_update", "final_update", "adamw", "grad_guard", "desc_upload", "stats")
+                "ns_update", "final_update", "adamw", "grad_guard", "desc_upload", "stats",
+                "embed_lookup", "embed_sort", "embed_grad", "ce_logits", "ce_rows", "ce_grad", "expert", "pack")
 
 
 class MuonError(RuntimeError):
@@ -192,6 +203,7 @@ def load_library(path: str = LIB_PATH):
         lib.muon_step_graph_launch.restype = ctypes.c_int
         lib.muon_step_graph_destroy.argtypes = [P]
         lib.muon_step_graph_destroy.restype = ctypes.c_int
+        train.declare(lib)
         _lib = lib
         return lib
 

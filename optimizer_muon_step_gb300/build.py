@@ -5,6 +5,7 @@ shared library next to this file.  Uses the shared CUDA runtime so the
 library and PyTorch share one runtime instance in a process."""
 from __future__ import annotations
 
+import glob
 import os
 import shutil
 import subprocess
@@ -17,7 +18,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libmuonstep.so")
-SOURCES = ["api.cu", "elementwise.cu", "ns_gemm.cu", "timing.cu", "noalloc.cu", "stats.cu", "adamw_multi.cu"]
+SOURCES = ["api.cu", "elementwise.cu", "ns_gemm.cu", "timing.cu", "noalloc.cu", "stats.cu", "adamw_multi.cu",
+           "embedding.cu", "train_gemm.cu", "cross_entropy.cu", "train_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -44,7 +46,7 @@ def _newer(target: str, deps) -> bool:
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
-    headers = [os.path.join(CSRC, "internal.h"), os.path.join(INCLUDE, "muon_step.h")]
+    headers = [*glob.glob(os.path.join(CSRC, "*.h")), os.path.join(INCLUDE, "muon_step.h")]
     objs, jobs = [], []
     for src in SOURCES:
         path = os.path.join(CSRC, src)

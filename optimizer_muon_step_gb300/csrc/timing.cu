@@ -156,6 +156,14 @@ const char* muon_kernel_name(int32_t kind) {
         case MUON_KERNEL_GRAD_GUARD: return "grad_guard";
         case MUON_KERNEL_DESC_UPLOAD: return "desc_upload";
         case MUON_KERNEL_STATS: return "stats";
+        case MUON_KERNEL_EMBED_LOOKUP: return "embed_lookup";
+        case MUON_KERNEL_EMBED_SORT: return "embed_sort";
+        case MUON_KERNEL_EMBED_GRAD: return "embed_grad";
+        case MUON_KERNEL_CE_LOGITS: return "ce_logits";
+        case MUON_KERNEL_CE_ROWS: return "ce_rows";
+        case MUON_KERNEL_CE_GRAD: return "ce_grad";
+        case MUON_KERNEL_EXPERT: return "expert";
+        case MUON_KERNEL_PACK: return "pack";
     }
     return "unknown";
 }

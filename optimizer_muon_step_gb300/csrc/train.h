@@ -1,0 +1,125 @@
+// Internal declarations of the operators around the step: the embedding, the
+// head's loss and the experts' products.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "internal.h"
+
+namespace muon {
+
+#ifdef __CUDACC__
+// Entry i of an int32 or int64 index array.
+__device__ __forceinline__ int64_t load_index(const void* p, int is64, int64_t i) {
+    return is64 ? static_cast<const int64_t*>(p)[i] : static_cast<int64_t>(static_cast<const int32_t*>(p)[i]);
+}
+
+// Element conversions by muon_dtype_t.
+template <int DT>
+struct Elem;
+template <>
+struct Elem<MUON_F32> {
+    typedef float T;
+    static __device__ __forceinline__ float load(T x) { return x; }
+    static __device__ __forceinline__ T store(float x) { return x; }
+};
+template <>
+struct Elem<MUON_BF16> {
+    typedef __nv_bfloat16 T;
+    static __device__ __forceinline__ float load(T x) { return __bfloat162float(x); }
+    static __device__ __forceinline__ T store(float x) { return __float2bfloat16_rn(x); }
+};
+template <>
+struct Elem<MUON_F16> {
+    typedef __half T;
+    static __device__ __forceinline__ float load(T x) { return __half2float(x); }
+    static __device__ __forceinline__ T store(float x) { return __float2half_rn(x); }
+};
+#endif
+
+inline size_t dtype_bytes(int dt) { return dt == MUON_F32 ? 4 : 2; }
+
+// ---- embedding (embedding.cu) ----------------------------------------------
+struct EmbedLookup {
+    const void* table;
+    const void* ids;
+    void* out;
+    int64_t table_ld, out_ld, vocab, dim, tokens, padding_idx;
+    int32_t table_dtype, out_dtype, ids64;
+    float scale;
+};
+cudaError_t launch_embed_lookup(const EmbedLookup& a, int num_sms, cudaStream_t st);
+
+struct EmbedGrad {
+    const void* grad;
+    const void* ids;
+    float* d_table;
+    int64_t grad_ld, vocab, dim, tokens, padding_idx;
+    int32_t grad_dtype, ids64, accumulate;
+    float scale;
+};
+size_t embed_grad_workspace(int64_t tokens, int64_t vocab, int64_t dim);
+cudaError_t launch_embed_grad(const EmbedGrad& a, void* workspace, int num_sms, cudaStream_t st);
+
+// ---- matrix products (train_gemm.cu) ---------------------------------------
+// C[M][N] = alpha * A B in fp32 sums over 16-bit operands.  A is [M][K]
+// row-major, or [K][M] with a_mn; B is [N][K], or [K][N] with b_mn.
+//   GROUP_M  M = all tokens' rows: rows of group e use B + e * b_stride
+//   GROUP_K  K = all tokens' rows: C + e * c_stride sums over group e's rows
+// with groups the ranges [offsets[e], offsets[e + 1]) of the token axis.
+enum { GROUP_NONE = 0, GROUP_M = 1, GROUP_K = 2 };
+
+struct TrainGemm {
+    const void* A;
+    const void* B;
+    void* C;
+    int64_t lda, ldb, ldc;  // elements
+    int64_t M, N, K;
+    int64_t b_stride, c_stride;  // elements, between groups
+    const void* offsets;
+    const float* alpha_dev;  // multiplies alpha when not null
+    int* status;
+    int64_t groups;
+    int32_t offsets64;
+    int32_t group;
+    int32_t dtype;       // of A and B
+    int32_t c_dtype;     // muon_dtype_t
+    int32_t accumulate;  // C += (fp32 only)
+    int32_t kind;        // muon_kernel_kind_t of the launch
+    bool a_mn, b_mn;
+    float alpha;
+};
+cudaError_t train_gemm(const TrainGemm& g, int num_sms, cudaStream_t st);
+
+// Copies rows of 2-byte elements to rows of another pitch.
+cudaError_t launch_pack(const void* src, int64_t src_ld, void* dst, int64_t dst_ld, int64_t rows, int64_t cols,
+                        int num_sms, cudaStream_t st);
+
+// ---- cross entropy rows (cross_entropy.cu) ---------------------------------
+struct CeRows {
+    const void* targets;
+    const float* row_scale;  // may be null
+    float* loss;
+    float* lse;
+    float* Z;          // block of logits, fp32, turned in place into the gradient's 16-bit rows
+    void* hidden;      // packed hidden rows of the block; ignored rows are cleared
+    const float* scale_max;  // device: largest |row_scale|
+    int* status;
+    int64_t z_ld, hidden_ld;
+    int64_t tokens, vocab, dim, ignore_index;
+    int32_t targets64, dtype, with_grad;
+    float logit_scale;
+};
+cudaError_t launch_ce_rows(const CeRows& r, cudaStream_t st);
+// out[0] = largest |row_scale| (1 when null), out[1] = out[0] * mult.
+cudaError_t launch_ce_scale(const float* row_scale, int64_t tokens, float mult, float* out, int* status,
+                            cudaStream_t st);
+// The fixed factor that keeps small fp16 logit gradients out of the
+// subnormal range: |g| <= 1 is stored times 2^15 (at most 32768 < 65504).
+// bf16 has fp32's exponents and takes 1.
+__host__ __device__ inline float ce_grad_lift(int dtype) { return dtype == MUON_F16 ? 32768.f : 1.f; }
+// dst = bf16 / fp16 (src), n elements.
+cudaError_t launch_round(const float* src, void* dst, int dtype, int64_t n, int num_sms, cudaStream_t st);
+
+}  // namespace muon

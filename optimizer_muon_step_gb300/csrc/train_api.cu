@@ -1,0 +1,573 @@
+// C ABI of the operators around the step: argument checks, workspace layout
+// and launch sequences.  Kernels live in embedding.cu, train_gemm.cu and
+// cross_entropy.cu.
+#include <math.h>
+
+#include <algorithm>
+#include <new>
+
+#include "host_checks.h"
+#include "train.h"
+
+using namespace muon;
+
+namespace {
+
+constexpr int64_t kMaxExtent = int64_t(1) << 30;  // extents are int32 tile coordinates in the products
+
+bool is_dtype(int32_t d) { return d == MUON_F32 || d == MUON_BF16 || d == MUON_F16; }
+bool is_half(int32_t d) { return d == MUON_BF16 || d == MUON_F16; }
+bool is_index(int32_t d) { return d == MUON_I32 || d == MUON_I64; }
+size_t index_bytes(int32_t d) { return d == MUON_I64 ? 8 : 4; }
+bool misaligned(const void* p, size_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
+
+// Bytes from the first element of `rows` rows to the end of the last one.
+size_t span(int64_t rows, int64_t cols, int64_t ld, size_t elem) {
+    return rows > 0 ? (static_cast<size_t>(rows - 1) * ld + cols) * elem : 0;
+}
+
+struct Buffer {
+    const void* p;
+    size_t bytes;
+    bool written;
+};
+
+// Written buffers overlap nothing; every buffer is the current device's
+// (left out while `st` is captured, like the step's own check).
+muon_status_t check_buffers(const Buffer* b, int n, cudaStream_t st) {
+    for (int i = 0; i < n; ++i) {
+        if (!b[i].written || b[i].bytes == 0) continue;
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(b[i].p), hi = lo + b[i].bytes;
+        for (int j = 0; j < n; ++j) {
+            if (j == i || b[j].bytes == 0) continue;
+            const uintptr_t l = reinterpret_cast<uintptr_t>(b[j].p);
+            if (l < hi && lo < l + b[j].bytes) return MUON_ERR_INVALID_ARG;
+        }
+    }
+    if (capturing(st)) return MUON_OK;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MUON_ERR_NO_DEVICE;
+    try {
+        DeviceMemoryCheck mem(dev);
+        for (int i = 0; i < n; ++i)
+            if (b[i].bytes > 0 && !mem.owns(b[i].p, b[i].bytes)) return MUON_ERR_INVALID_ARG;
+    } catch (const std::bad_alloc&) {
+        return MUON_ERR_CUDA;
+    }
+    return MUON_OK;
+}
+
+muon_status_t check_workspace(const void* workspace, size_t ws_bytes, size_t need) {
+    if (need == 0 || !workspace) return MUON_ERR_INVALID_ARG;
+    if (misaligned(workspace, 256)) return MUON_ERR_MISALIGNED;
+    return ws_bytes < need ? MUON_ERR_WORKSPACE_TOO_SMALL : MUON_OK;
+}
+
+// Whether a 16-bit matrix can be copied to shared memory by tensor copies as
+// it stands: 16-byte base and rows.  Others are packed first.
+bool tma_ready(const void* p, int64_t ld) { return !misaligned(p, 16) && ld % 8 == 0; }
+
+int64_t pitch8(int64_t cols) { return round_up(cols, 8); }
+
+size_t packed_bytes(int64_t rows, int64_t cols) {
+    return static_cast<size_t>(round_up(2 * rows * pitch8(cols), 256));
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// Embedding
+// ---------------------------------------------------------------------------
+extern "C" {
+
+muon_status_t muon_embedding_lookup(const void* table, int32_t table_dtype, int64_t table_ld, int64_t vocab,
+                                    int64_t dim, const void* ids, int32_t ids_dtype, int64_t tokens, float scale,
+                                    int64_t padding_idx, void* out, int32_t out_dtype, int64_t out_ld, void* stream) {
+    NvtxScope range("muon_embedding_lookup");
+    if (!is_dtype(table_dtype) || !is_dtype(out_dtype) || !is_index(ids_dtype)) return MUON_ERR_UNSUPPORTED_DTYPE;
+    if (tokens < 0 || vocab <= 0 || dim <= 0 || table_ld < dim || out_ld < dim || vocab >= (int64_t(1) << 31) ||
+        tokens >= (int64_t(1) << 31) || dim > kMaxExtent || table_ld > kMaxExtent || out_ld > kMaxExtent)
+        return MUON_ERR_INVALID_ARG;
+    if (tokens == 0) return MUON_OK;
+    if (!table || !ids || !out) return MUON_ERR_INVALID_ARG;
+    const size_t te = dtype_bytes(table_dtype), oe = dtype_bytes(out_dtype), ie = index_bytes(ids_dtype);
+    if (misaligned(table, te) || misaligned(out, oe) || misaligned(ids, ie)) return MUON_ERR_MISALIGNED;
+    int num_sms = 0;
+    muon_status_t s = device_info(&num_sms);
+    if (s != MUON_OK) return s;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const Buffer b[] = {{table, span(vocab, dim, table_ld, te), false},
+                        {ids, static_cast<size_t>(tokens) * ie, false},
+                        {out, span(tokens, dim, out_ld, oe), true}};
+    s = check_buffers(b, 3, st);
+    if (s != MUON_OK) return s;
+    EmbedLookup a;
+    a.table = table;
+    a.ids = ids;
+    a.out = out;
+    a.table_ld = table_ld;
+    a.out_ld = out_ld;
+    a.vocab = vocab;
+    a.dim = dim;
+    a.tokens = tokens;
+    a.padding_idx = padding_idx;
+    a.table_dtype = table_dtype;
+    a.out_dtype = out_dtype;
+    a.ids64 = ids_dtype == MUON_I64;
+    a.scale = scale;
+    return from_cuda(launch_embed_lookup(a, num_sms, st));
+}
+
+size_t muon_embedding_grad_workspace(int64_t tokens, int64_t vocab, int64_t dim) {
+    if (tokens < 0 || vocab <= 0 || dim <= 0 || vocab >= (int64_t(1) << 31) || tokens >= (int64_t(1) << 31) ||
+        dim > kMaxExtent)
+        return 0;
+    return embed_grad_workspace(tokens, vocab, dim);
+}
+
+muon_status_t muon_embedding_grad(const void* grad, int32_t grad_dtype, int64_t grad_ld, const void* ids,
+                                  int32_t ids_dtype, int64_t tokens, int64_t vocab, int64_t dim, float scale,
+                                  int64_t padding_idx, int32_t accumulate, float* d_table, void* workspace,
+                                  size_t ws_bytes, void* stream) {
+    NvtxScope range("muon_embedding_grad");
+    if (!is_dtype(grad_dtype) || !is_index(ids_dtype)) return MUON_ERR_UNSUPPORTED_DTYPE;
+    const size_t need = muon_embedding_grad_workspace(tokens, vocab, dim);
+    if (need == 0 || grad_ld < dim || grad_ld > kMaxExtent || (accumulate != 0 && accumulate != 1))
+        return MUON_ERR_INVALID_ARG;
+    if (!d_table || (tokens > 0 && (!grad || !ids))) return MUON_ERR_INVALID_ARG;
+    const size_t ge = dtype_bytes(grad_dtype), ie = index_bytes(ids_dtype);
+    if (misaligned(d_table, 4) || misaligned(grad, ge) || misaligned(ids, ie)) return MUON_ERR_MISALIGNED;
+    muon_status_t s = check_workspace(workspace, ws_bytes, need);
+    if (s != MUON_OK) return s;
+    int num_sms = 0;
+    s = device_info(&num_sms);
+    if (s != MUON_OK) return s;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const Buffer b[] = {{grad, span(tokens, dim, grad_ld, ge), false},
+                        {ids, static_cast<size_t>(tokens) * ie, false},
+                        {d_table, static_cast<size_t>(vocab) * dim * 4, true},
+                        {workspace, need, true}};
+    s = check_buffers(b, 4, st);
+    if (s != MUON_OK) return s;
+    EmbedGrad a;
+    a.grad = grad;
+    a.ids = ids;
+    a.d_table = d_table;
+    a.grad_ld = grad_ld;
+    a.vocab = vocab;
+    a.dim = dim;
+    a.tokens = tokens;
+    a.padding_idx = padding_idx;
+    a.grad_dtype = grad_dtype;
+    a.ids64 = ids_dtype == MUON_I64;
+    a.accumulate = accumulate;
+    a.scale = scale;
+    return from_cuda(launch_embed_grad(a, workspace, num_sms, st));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Cross entropy of the head
+// ---------------------------------------------------------------------------
+namespace {
+
+// Workspace: header and scalars, the packed weight (when its rows are not
+// 16-byte), the fp32 sums of d_weight (several blocks and a 16-bit result),
+// then per token of a block: the packed hidden row and the row of logits.
+struct CeLayout {
+    int64_t block = 0;   // tokens per block
+    int64_t z_ld = 0, h_ld = 0, w_ld = 0;
+    bool pack_w = false, sums = false;
+    size_t w_off = 0, sum_off = 0, h_off = 0, z_off = 0, total = 0;
+};
+
+constexpr size_t kScalarsOff = 256;
+constexpr size_t kFixedBytes = 512;
+
+size_t ce_total(const muon_linear_ce_t* p, bool grad, int64_t block, CeLayout* L) {
+    const int64_t v = p->vocab, d = p->dim;
+    L->block = block;
+    L->z_ld = round_up(v, 64);
+    L->h_ld = pitch8(d);
+    L->pack_w = !tma_ready(p->weight, p->weight_ld);
+    L->w_ld = L->pack_w ? pitch8(d) : p->weight_ld;
+    L->sums = grad && block < p->tokens && p->d_weight_dtype != MUON_F32;
+    size_t at = kFixedBytes;
+    L->w_off = at;
+    if (L->pack_w) at += packed_bytes(v, d);
+    L->sum_off = at;
+    if (L->sums) at += static_cast<size_t>(round_up(4 * v * d, 256));
+    L->h_off = at;
+    at += packed_bytes(block, d);
+    L->z_off = at;
+    at += static_cast<size_t>(4 * block * L->z_ld);
+    L->total = at;
+    return at;
+}
+
+bool ce_sizes_ok(const muon_linear_ce_t* p) {
+    return p && p->tokens >= 0 && p->vocab > 0 && p->dim > 0 && p->tokens < kMaxExtent && p->vocab < kMaxExtent &&
+           p->dim < kMaxExtent && p->hidden_ld >= p->dim && p->weight_ld >= p->dim && p->hidden_ld < kMaxExtent &&
+           p->weight_ld < kMaxExtent;
+}
+
+// The largest block of tokens (all of them, or a multiple of 256) that
+// `bytes` holds; 0 when not even 256 fit.
+int64_t ce_block(const muon_linear_ce_t* p, bool grad, size_t bytes, CeLayout* L) {
+    if (ce_total(p, grad, p->tokens, L) <= bytes) return p->tokens;
+    int64_t lo = 0, hi = p->tokens / 256;  // blocks of lo * 256 fit
+    while (lo < hi) {
+        const int64_t mid = (lo + hi + 1) / 2;
+        if (ce_total(p, grad, 256 * mid, L) <= bytes) lo = mid;
+        else hi = mid - 1;
+    }
+    if (lo == 0) return 0;
+    ce_total(p, grad, 256 * lo, L);
+    return 256 * lo;
+}
+
+muon_status_t ce_run(const muon_linear_ce_t* p, bool grad, void* workspace, size_t ws_bytes, void* stream) {
+    if (!p || p->reserved != 0) return MUON_ERR_INVALID_ARG;
+    if (!is_half(p->dtype) || !is_index(p->targets_dtype)) return MUON_ERR_UNSUPPORTED_DTYPE;
+    if (!ce_sizes_ok(p) || !isfinite(p->logit_scale)) return MUON_ERR_INVALID_ARG;
+    const int64_t n = p->tokens, v = p->vocab, d = p->dim;
+    const size_t ie = index_bytes(p->targets_dtype);
+    if (n > 0 && (!p->hidden || !p->weight || !p->targets || !p->loss || !p->lse)) return MUON_ERR_INVALID_ARG;
+    if (misaligned(p->hidden, 2) || misaligned(p->weight, 2) || misaligned(p->targets, ie) ||
+        misaligned(p->loss, 4) || misaligned(p->lse, 4))
+        return MUON_ERR_MISALIGNED;
+    size_t we = 0;
+    if (grad) {
+        if (p->d_weight_dtype != p->dtype && p->d_weight_dtype != MUON_F32) return MUON_ERR_UNSUPPORTED_DTYPE;
+        if (p->accumulate != 0 && (p->accumulate != 1 || p->d_weight_dtype != MUON_F32)) return MUON_ERR_INVALID_ARG;
+        if (!p->d_weight || (n > 0 && !p->d_hidden)) return MUON_ERR_INVALID_ARG;
+        we = dtype_bytes(p->d_weight_dtype);
+        if (misaligned(p->row_scale, 4) || misaligned(p->d_hidden, 2) || misaligned(p->d_weight, we))
+            return MUON_ERR_MISALIGNED;
+    }
+    if (n == 0 && !grad) return MUON_OK;
+    muon_status_t s = check_workspace(workspace, ws_bytes, kFixedBytes);
+    if (s != MUON_OK) return s;
+    CeLayout L;
+    const int64_t block = n > 0 ? ce_block(p, grad, ws_bytes, &L) : 0;
+    if (n > 0 && block == 0) return MUON_ERR_WORKSPACE_TOO_SMALL;
+    int num_sms = 0;
+    s = device_info(&num_sms);
+    if (s != MUON_OK) return s;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const size_t vd = static_cast<size_t>(v) * d;
+    const Buffer b[] = {{p->hidden, span(n, d, p->hidden_ld, 2), false},
+                        {p->weight, n > 0 ? span(v, d, p->weight_ld, 2) : 0, false},
+                        {p->targets, static_cast<size_t>(n) * ie, false},
+                        {p->loss, static_cast<size_t>(n) * 4, true},
+                        {p->lse, static_cast<size_t>(n) * 4, true},
+                        {workspace, n > 0 ? L.total : kFixedBytes, true},
+                        {grad ? p->row_scale : nullptr, grad && p->row_scale ? static_cast<size_t>(n) * 4 : 0, false},
+                        {p->d_hidden, grad ? static_cast<size_t>(n) * d * 2 : 0, true},
+                        {p->d_weight, grad ? vd * we : 0, true}};
+    s = check_buffers(b, 9, st);
+    if (s != MUON_OK) return s;
+    if (n == 0) {
+        if (p->accumulate) return MUON_OK;
+        return from_cuda(cudaMemsetAsync(p->d_weight, 0, vd * we, st));
+    }
+
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    int* status = reinterpret_cast<int*>(ws);
+    float* scalars = reinterpret_cast<float*>(ws + kScalarsOff);
+    cudaError_t e = launch_ce_scale(grad ? p->row_scale : nullptr, n, p->logit_scale / ce_grad_lift(p->dtype), scalars,
+                                    status, st);
+    const void* weight = p->weight;
+    if (e == cudaSuccess && L.pack_w) {
+        e = launch_pack(p->weight, p->weight_ld, ws + L.w_off, L.w_ld, v, d, num_sms, st);
+        weight = ws + L.w_off;
+    }
+    for (int64_t t0 = 0; t0 < n && e == cudaSuccess; t0 += block) {
+        const int64_t m = std::min(block, n - t0);
+        const uint8_t* hidden = static_cast<const uint8_t*>(p->hidden) + 2 * t0 * p->hidden_ld;
+        float* Z = reinterpret_cast<float*>(ws + L.z_off);
+        void* H = ws + L.h_off;
+        e = launch_pack(hidden, p->hidden_ld, H, L.h_ld, m, d, num_sms, st);
+        if (e != cudaSuccess) break;
+        TrainGemm g = {};
+        g.A = H;
+        g.lda = L.h_ld;
+        g.B = weight;
+        g.ldb = L.w_ld;
+        g.C = Z;
+        g.ldc = L.z_ld;
+        g.c_dtype = MUON_F32;
+        g.M = m;
+        g.N = v;
+        g.K = d;
+        g.alpha = 1.f;
+        g.dtype = p->dtype;
+        g.kind = MUON_KERNEL_CE_LOGITS;
+        e = train_gemm(g, num_sms, st);
+        if (e != cudaSuccess) break;
+        CeRows r = {};
+        r.targets = static_cast<const uint8_t*>(p->targets) + t0 * ie;
+        r.row_scale = grad && p->row_scale ? p->row_scale + t0 : nullptr;
+        r.loss = p->loss + t0;
+        r.lse = p->lse + t0;
+        r.Z = Z;
+        r.z_ld = L.z_ld;
+        r.hidden = H;
+        r.hidden_ld = L.h_ld;
+        r.scale_max = scalars;
+        r.status = status;
+        r.tokens = m;
+        r.vocab = v;
+        r.dim = d;
+        r.ignore_index = p->ignore_index;
+        r.targets64 = p->targets_dtype == MUON_I64;
+        r.dtype = p->dtype;
+        r.with_grad = grad;
+        r.logit_scale = p->logit_scale;
+        e = launch_ce_rows(r, st);
+        if (e != cudaSuccess || !grad) continue;
+        // d_hidden = G W; the rows of G lie in the front halves of Z's rows
+        g = TrainGemm{};
+        g.A = Z;
+        g.lda = 2 * L.z_ld;
+        g.B = weight;
+        g.ldb = L.w_ld;
+        g.b_mn = true;
+        g.C = static_cast<uint8_t*>(p->d_hidden) + 2 * t0 * d;
+        g.ldc = d;
+        g.c_dtype = p->dtype;
+        g.M = m;
+        g.N = d;
+        g.K = v;
+        g.alpha = 1.f;
+        g.alpha_dev = scalars + 1;
+        g.dtype = p->dtype;
+        g.kind = MUON_KERNEL_CE_GRAD;
+        e = train_gemm(g, num_sms, st);
+        if (e != cudaSuccess) break;
+        // d_weight += G^T H
+        g = TrainGemm{};
+        g.A = Z;
+        g.lda = 2 * L.z_ld;
+        g.a_mn = true;
+        g.B = H;
+        g.ldb = L.h_ld;
+        g.b_mn = true;
+        g.C = L.sums ? static_cast<void*>(ws + L.sum_off) : p->d_weight;
+        g.ldc = d;
+        g.c_dtype = L.sums ? static_cast<int32_t>(MUON_F32) : p->d_weight_dtype;
+        g.accumulate = t0 > 0 || p->accumulate;
+        g.M = v;
+        g.N = d;
+        g.K = m;
+        g.alpha = 1.f;
+        g.alpha_dev = scalars + 1;
+        g.dtype = p->dtype;
+        g.kind = MUON_KERNEL_CE_GRAD;
+        e = train_gemm(g, num_sms, st);
+    }
+    if (e == cudaSuccess && L.sums)
+        e = launch_round(reinterpret_cast<const float*>(ws + L.sum_off), p->d_weight, p->dtype,
+                         static_cast<int64_t>(vd), num_sms, st);
+    return from_cuda(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t muon_linear_ce_workspace(const muon_linear_ce_t* p, int32_t with_grad, size_t budget_bytes) {
+    if (!ce_sizes_ok(p)) return 0;
+    CeLayout L;
+    if (p->tokens == 0) return kFixedBytes;
+    if (ce_block(p, with_grad != 0, budget_bytes, &L) > 0) return L.total;
+    return ce_total(p, with_grad != 0, std::min<int64_t>(256, p->tokens), &L);
+}
+
+muon_status_t muon_linear_ce(const muon_linear_ce_t* p, void* workspace, size_t ws_bytes, void* stream) {
+    NvtxScope range("muon_linear_ce");
+    return ce_run(p, false, workspace, ws_bytes, stream);
+}
+
+muon_status_t muon_linear_ce_grad(const muon_linear_ce_t* p, void* workspace, size_t ws_bytes, void* stream) {
+    NvtxScope range("muon_linear_ce_grad");
+    return ce_run(p, true, workspace, ws_bytes, stream);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Products grouped by expert
+// ---------------------------------------------------------------------------
+namespace {
+
+bool expert_sizes_ok(int64_t experts, int64_t tokens, int64_t rows, int64_t cols) {
+    return experts > 0 && experts <= 65536 && tokens >= 0 && tokens < kMaxExtent && rows > 0 && rows < kMaxExtent &&
+           cols > 0 && cols < kMaxExtent && experts * rows < (int64_t(1) << 31) * 8;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t muon_expert_matmul_workspace(const void* x, int64_t x_ld, const void* weight, int64_t experts, int64_t tokens,
+                                    int64_t rows, int64_t cols, int32_t transpose) {
+    if (!expert_sizes_ok(experts, tokens, rows, cols)) return 0;
+    size_t n = kHeaderBytes;
+    if (!tma_ready(x, x_ld)) n += packed_bytes(tokens, transpose ? rows : cols);
+    if (!tma_ready(weight, cols)) n += packed_bytes(experts * rows, cols);
+    return n;
+}
+
+muon_status_t muon_expert_matmul(const void* x, int64_t x_ld, const void* weight, const void* offsets,
+                                 int32_t offsets_dtype, int32_t dtype, int64_t experts, int64_t tokens, int64_t rows,
+                                 int64_t cols, int32_t transpose, void* y, int64_t y_ld, void* workspace,
+                                 size_t ws_bytes, void* stream) {
+    NvtxScope range("muon_expert_matmul");
+    if (!is_half(dtype) || !is_index(offsets_dtype)) return MUON_ERR_UNSUPPORTED_DTYPE;
+    if (!expert_sizes_ok(experts, tokens, rows, cols) || (transpose != 0 && transpose != 1))
+        return MUON_ERR_INVALID_ARG;
+    const int64_t xc = transpose ? rows : cols, yc = transpose ? cols : rows;
+    if (x_ld < xc || y_ld < yc || x_ld >= kMaxExtent || y_ld >= kMaxExtent) return MUON_ERR_INVALID_ARG;
+    if (tokens == 0) return MUON_OK;
+    if (!x || !weight || !offsets || !y) return MUON_ERR_INVALID_ARG;
+    if (misaligned(x, 2) || misaligned(weight, 2) || misaligned(y, 2) || misaligned(offsets, index_bytes(offsets_dtype)))
+        return MUON_ERR_MISALIGNED;
+    const size_t need = muon_expert_matmul_workspace(x, x_ld, weight, experts, tokens, rows, cols, transpose);
+    muon_status_t s = check_workspace(workspace, ws_bytes, need);
+    if (s != MUON_OK) return s;
+    int num_sms = 0;
+    s = device_info(&num_sms);
+    if (s != MUON_OK) return s;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const Buffer b[] = {{x, span(tokens, xc, x_ld, 2), false},
+                        {weight, static_cast<size_t>(experts) * rows * cols * 2, false},
+                        {offsets, static_cast<size_t>(experts + 1) * index_bytes(offsets_dtype), false},
+                        {y, span(tokens, yc, y_ld, 2), true},
+                        {workspace, need, true}};
+    s = check_buffers(b, 5, st);
+    if (s != MUON_OK) return s;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    uint8_t* at = ws + kHeaderBytes;
+    TrainGemm g = {};
+    g.A = x;
+    g.lda = x_ld;
+    g.B = weight;
+    g.ldb = cols;
+    cudaError_t e = cudaSuccess;
+    if (!tma_ready(x, x_ld)) {
+        e = launch_pack(x, x_ld, at, pitch8(xc), tokens, xc, num_sms, st);
+        g.A = at;
+        g.lda = pitch8(xc);
+        at += packed_bytes(tokens, xc);
+    }
+    if (e == cudaSuccess && !tma_ready(weight, cols)) {
+        e = launch_pack(weight, cols, at, pitch8(cols), experts * rows, cols, num_sms, st);
+        g.B = at;
+        g.ldb = pitch8(cols);
+    }
+    if (e != cudaSuccess) return from_cuda(e);
+    g.b_mn = transpose != 0;
+    g.b_stride = rows * g.ldb;
+    g.C = y;
+    g.ldc = y_ld;
+    g.c_dtype = dtype;
+    g.M = tokens;
+    g.N = yc;
+    g.K = xc;
+    g.group = GROUP_M;
+    g.groups = experts;
+    g.offsets = offsets;
+    g.offsets64 = offsets_dtype == MUON_I64;
+    g.alpha = 1.f;
+    g.dtype = dtype;
+    g.status = reinterpret_cast<int*>(ws);
+    g.kind = MUON_KERNEL_EXPERT;
+    return from_cuda(train_gemm(g, num_sms, st));
+}
+
+size_t muon_expert_wgrad_workspace(const void* grad, int64_t grad_ld, const void* x, int64_t x_ld, int64_t experts,
+                                   int64_t tokens, int64_t rows, int64_t cols) {
+    if (!expert_sizes_ok(experts, tokens, rows, cols)) return 0;
+    size_t n = kHeaderBytes;
+    if (!tma_ready(grad, grad_ld)) n += packed_bytes(tokens, rows);
+    if (!tma_ready(x, x_ld)) n += packed_bytes(tokens, cols);
+    return n;
+}
+
+muon_status_t muon_expert_wgrad(const void* grad, int64_t grad_ld, const void* x, int64_t x_ld, const void* offsets,
+                                int32_t offsets_dtype, int32_t dtype, int64_t experts, int64_t tokens, int64_t rows,
+                                int64_t cols, void* d_weight, int32_t d_weight_dtype, int32_t accumulate,
+                                void* workspace, size_t ws_bytes, void* stream) {
+    NvtxScope range("muon_expert_wgrad");
+    if (!is_half(dtype) || !is_index(offsets_dtype) || (d_weight_dtype != dtype && d_weight_dtype != MUON_F32))
+        return MUON_ERR_UNSUPPORTED_DTYPE;
+    if (!expert_sizes_ok(experts, tokens, rows, cols) || grad_ld < rows || x_ld < cols || grad_ld >= kMaxExtent ||
+        x_ld >= kMaxExtent)
+        return MUON_ERR_INVALID_ARG;
+    if (accumulate != 0 && (accumulate != 1 || d_weight_dtype != MUON_F32)) return MUON_ERR_INVALID_ARG;
+    if (!d_weight || (tokens > 0 && (!grad || !x || !offsets))) return MUON_ERR_INVALID_ARG;
+    const size_t we = dtype_bytes(d_weight_dtype), ie = index_bytes(offsets_dtype);
+    if (misaligned(grad, 2) || misaligned(x, 2) || misaligned(d_weight, we) || misaligned(offsets, ie))
+        return MUON_ERR_MISALIGNED;
+    const size_t need = muon_expert_wgrad_workspace(grad, grad_ld, x, x_ld, experts, tokens, rows, cols);
+    muon_status_t s = check_workspace(workspace, ws_bytes, need);
+    if (s != MUON_OK) return s;
+    int num_sms = 0;
+    s = device_info(&num_sms);
+    if (s != MUON_OK) return s;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const size_t dw_bytes = static_cast<size_t>(experts) * rows * cols * we;
+    const Buffer b[] = {{grad, span(tokens, rows, grad_ld, 2), false},
+                        {x, span(tokens, cols, x_ld, 2), false},
+                        {offsets, tokens > 0 ? static_cast<size_t>(experts + 1) * ie : 0, false},
+                        {d_weight, dw_bytes, true},
+                        {workspace, need, true}};
+    s = check_buffers(b, 5, st);
+    if (s != MUON_OK) return s;
+    if (tokens == 0) {
+        if (accumulate) return MUON_OK;
+        return from_cuda(cudaMemsetAsync(d_weight, 0, dw_bytes, st));
+    }
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    uint8_t* at = ws + kHeaderBytes;
+    TrainGemm g = {};
+    g.A = grad;
+    g.lda = grad_ld;
+    g.B = x;
+    g.ldb = x_ld;
+    cudaError_t e = cudaSuccess;
+    if (!tma_ready(grad, grad_ld)) {
+        e = launch_pack(grad, grad_ld, at, pitch8(rows), tokens, rows, num_sms, st);
+        g.A = at;
+        g.lda = pitch8(rows);
+        at += packed_bytes(tokens, rows);
+    }
+    if (e == cudaSuccess && !tma_ready(x, x_ld)) {
+        e = launch_pack(x, x_ld, at, pitch8(cols), tokens, cols, num_sms, st);
+        g.B = at;
+        g.ldb = pitch8(cols);
+    }
+    if (e != cudaSuccess) return from_cuda(e);
+    g.a_mn = g.b_mn = true;
+    g.C = d_weight;
+    g.ldc = cols;
+    g.c_stride = rows * cols;
+    g.c_dtype = d_weight_dtype;
+    g.accumulate = accumulate;
+    g.M = rows;
+    g.N = cols;
+    g.K = tokens;
+    g.group = GROUP_K;
+    g.groups = experts;
+    g.offsets = offsets;
+    g.offsets64 = offsets_dtype == MUON_I64;
+    g.alpha = 1.f;
+    g.dtype = dtype;
+    g.status = reinterpret_cast<int*>(ws);
+    g.kind = MUON_KERNEL_EXPERT;
+    return from_cuda(train_gemm(g, num_sms, st));
+}
+
+}  // extern "C"

@@ -1,0 +1,313 @@
+"""The operators around the step: embedding, head loss, experts' products.
+
+Marshalling only, like the rest of the binding; the semantics, layouts and
+errors are those of ``include/muon_step.h``.  Matrices may have any row
+pitch (their last dimension must be contiguous).  Outputs and workspaces
+that are not given are allocated by torch on the stream of the call.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+
+_P = ctypes.c_void_p
+
+
+class LinearCe(ctypes.Structure):
+    _fields_ = [("hidden", _P), ("weight", _P), ("targets", _P), ("loss", _P), ("lse", _P),
+                ("tokens", ctypes.c_int64), ("vocab", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("hidden_ld", ctypes.c_int64), ("weight_ld", ctypes.c_int64), ("ignore_index", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("targets_dtype", ctypes.c_int32), ("logit_scale", ctypes.c_float),
+                ("d_weight_dtype", ctypes.c_int32), ("row_scale", _P), ("d_hidden", _P), ("d_weight", _P),
+                ("accumulate", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+def declare(lib):
+    """Argument types of this module's entry points."""
+    i64, i32, f32, size = ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
+    for name, args, res in (
+            ("muon_embedding_lookup", [_P, i32, i64, i64, i64, _P, i32, i64, f32, i64, _P, i32, i64, _P], ctypes.c_int),
+            ("muon_embedding_grad_workspace", [i64, i64, i64], size),
+            ("muon_embedding_grad", [_P, i32, i64, _P, i32, i64, i64, i64, f32, i64, i32, _P, _P, size, _P],
+             ctypes.c_int),
+            ("muon_linear_ce_workspace", [_P, i32, size], size),
+            ("muon_linear_ce", [_P, _P, size, _P], ctypes.c_int),
+            ("muon_linear_ce_grad", [_P, _P, size, _P], ctypes.c_int),
+            ("muon_expert_matmul_workspace", [_P, i64, _P, i64, i64, i64, i64, i32], size),
+            ("muon_expert_matmul", [_P, i64, _P, _P, i32, i32, i64, i64, i64, i64, i32, _P, i64, _P, size, _P],
+             ctypes.c_int),
+            ("muon_expert_wgrad_workspace", [_P, i64, _P, i64, i64, i64, i64, i64], size),
+            ("muon_expert_wgrad", [_P, i64, _P, i64, _P, i32, i32, i64, i64, i64, i64, _P, i32, i32, _P, size, _P],
+             ctypes.c_int)):
+        f = getattr(lib, name)
+        f.argtypes, f.restype = args, res
+
+
+EXPORTS = ("muon_embedding_lookup", "muon_embedding_grad_workspace", "muon_embedding_grad",
+           "muon_linear_ce_workspace", "muon_linear_ce", "muon_linear_ce_grad", "muon_expert_matmul_workspace",
+           "muon_expert_matmul", "muon_expert_wgrad_workspace", "muon_expert_wgrad")
+
+
+def _pkg():
+    import optimizer_muon_step_gb300 as m
+    return m
+
+
+def _dtypes():
+    import torch
+    return {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def _rows(t, name, dtypes, cols=None, rows=None):
+    """A CUDA matrix whose rows are contiguous; its row pitch."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
+    if t.dim() != 2 or (cols is not None and t.shape[1] != cols) or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name} must be a matrix of shape ({rows or 'any'}, {cols or 'any'}), got {tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if t.shape[0] <= 1:
+        return t.shape[1]
+    if t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name} must have rows that do not overlap")
+    return t.stride(0)
+
+
+def _index(t, name, n=None):
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"{name} has dtype {t.dtype}, expected int32 or int64")
+    if not t.is_contiguous() or (n is not None and t.numel() != n):
+        raise ValueError(f"{name} must be contiguous" + (f" with {n} entries" if n is not None else ""))
+    return 1 if t.dtype == torch.int64 else 0
+
+
+def _out(t, name, shape, dtypes, device):
+    """`t` checked as a contiguous output of `shape`, or a new one of dtypes[0]."""
+    import torch
+    if t is None:
+        return torch.empty(shape, dtype=dtypes[0], device=device)
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in dtypes:
+        raise TypeError(f"{name} must be a CUDA tensor of dtype {' or '.join(map(str, dtypes))}")
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _on(stream):
+    """Makes `stream` (None: the current one) torch's allocation stream, so
+    that outputs and workspaces made inside belong to it."""
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
+def _workspace(workspace, need, where, device):
+    m = _pkg()
+    if need == 0:
+        raise m.MuonError(1, where)
+    return m.allocate_workspace(need, device) if workspace is None else workspace
+
+
+def muon_embedding_lookup(table, ids, scale: float = 1.0, padding_idx=None, out=None, out_dtype=None, stream=None):
+    """scale * table[ids], rounded once to `out_dtype` (default: the table's).
+
+    table: (vocab, dim) fp32, bf16 or fp16; ids: int32 or int64 of any shape.
+    Ids equal to `padding_idx`, and ids outside the table, give zero rows."""
+    m = _pkg()
+    dts = _dtypes()
+    ld = _rows(table, "table", dts)
+    is64 = _index(ids, "ids")
+    vocab, dim = table.shape
+    with _on(stream):
+        if out is None:
+            out = table.new_empty((*ids.shape, dim), dtype=out_dtype or table.dtype)
+            o, old = out, dim
+        else:
+            o = out if out.dim() == 2 else out.view(-1, dim)
+            old = _rows(o, "out", dts, dim, ids.numel())
+        m._check(m.load_library().muon_embedding_lookup(
+            table.data_ptr(), dts[table.dtype], ld, vocab, dim, ids.data_ptr(), is64, ids.numel(), scale,
+            -1 if padding_idx is None else int(padding_idx), o.data_ptr(), dts[o.dtype], old, m._stream(stream)),
+            "muon_embedding_lookup")
+    return out
+
+
+def muon_embedding_grad(grad, ids, vocab: int, scale: float = 1.0, padding_idx=None, out=None,
+                        accumulate: bool = False, workspace=None, stream=None):
+    """The lookup's gradient as a dense fp32 (vocab, dim) table: row v is
+    scale * the sum of `grad`'s rows whose id is v (added to `out` with
+    `accumulate`).  grad: (*ids.shape, dim) or (tokens, dim)."""
+    import torch
+    m = _pkg()
+    dts = _dtypes()
+    is64 = _index(ids, "ids")
+    g = grad if grad.dim() == 2 else grad.reshape(-1, grad.shape[-1])
+    ld = _rows(g, "grad", dts, None, ids.numel())
+    dim = g.shape[1]
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    with _on(stream):
+        out = _out(out, "out", (int(vocab), dim), (torch.float32,), g.device)
+        lib = m.load_library()
+        ws = _workspace(workspace, lib.muon_embedding_grad_workspace(ids.numel(), int(vocab), dim),
+                        "muon_embedding_grad", g.device)
+        m._check(lib.muon_embedding_grad(g.data_ptr(), dts[g.dtype], ld, ids.data_ptr(), is64, ids.numel(), int(vocab),
+                                         dim, scale, -1 if padding_idx is None else int(padding_idx),
+                                         int(bool(accumulate)), out.data_ptr(), ws.data_ptr(), ws.numel(),
+                                         m._stream(stream)), "muon_embedding_grad")
+    return out
+
+
+def _ce_struct(hidden, weight, targets, logit_scale, ignore_index):
+    import torch
+    dts = _dtypes()
+    half = (torch.bfloat16, torch.float16)
+    hld = _rows(hidden, "hidden", half)
+    n, d = hidden.shape
+    wld = _rows(weight, "weight", (hidden.dtype,), d)
+    p = LinearCe()
+    p.hidden, p.weight, p.targets = hidden.data_ptr(), weight.data_ptr(), targets.data_ptr()
+    p.tokens, p.vocab, p.dim = n, weight.shape[0], d
+    p.hidden_ld, p.weight_ld = hld, wld
+    p.ignore_index = int(ignore_index)
+    p.dtype = p.d_weight_dtype = dts[hidden.dtype]
+    p.targets_dtype = _index(targets, "targets", n)
+    p.logit_scale = float(logit_scale)
+    return p
+
+
+def muon_linear_ce_workspace(hidden, weight, targets, with_grad: bool, budget_bytes: int = 8 << 30) -> int:
+    """Workspace bytes of muon_linear_ce or (with_grad) muon_linear_ce_grad."""
+    p = _ce_struct(hidden, weight, targets, 1.0, -1)
+    return int(_pkg().load_library().muon_linear_ce_workspace(ctypes.addressof(p), int(bool(with_grad)),
+                                                              int(budget_bytes)))
+
+
+def muon_linear_ce(hidden, weight, targets, logit_scale: float = 1.0, ignore_index: int = -100, loss=None, lse=None,
+                   workspace=None, budget_bytes: int = 8 << 30, stream=None):
+    """(loss, lse), fp32 per token, of the softmax over logit_scale * hidden
+    weight^T.  hidden: (tokens, dim), weight: (vocab, dim), both bf16 or
+    both fp16; targets: int32 or int64.  Ignored tokens have loss 0."""
+    import torch
+    m = _pkg()
+    p = _ce_struct(hidden, weight, targets, logit_scale, ignore_index)
+    with _on(stream):
+        loss = _out(loss, "loss", (p.tokens,), (torch.float32,), hidden.device)
+        lse = _out(lse, "lse", (p.tokens,), (torch.float32,), hidden.device)
+        p.loss, p.lse = loss.data_ptr(), lse.data_ptr()
+        lib = m.load_library()
+        at = ctypes.addressof(p)
+        ws = workspace
+        if ws is None:
+            ws = _workspace(None, lib.muon_linear_ce_workspace(at, 0, int(budget_bytes)), "muon_linear_ce",
+                            hidden.device)
+        m._check(lib.muon_linear_ce(at, ws.data_ptr(), ws.numel(), m._stream(stream)), "muon_linear_ce")
+    return loss, lse
+
+
+def muon_linear_ce_grad(hidden, weight, targets, row_scale=None, logit_scale: float = 1.0, ignore_index: int = -100,
+                        loss=None, lse=None, d_hidden=None, d_weight=None, accumulate: bool = False, workspace=None,
+                        budget_bytes: int = 8 << 30, stream=None):
+    """(loss, lse, d_hidden, d_weight): muon_linear_ce's results and the
+    gradients of sum(row_scale * loss).  row_scale: fp32 per token, e.g. 1 /
+    (number of counted tokens) for the mean; None means 1.  `d_weight` may be
+    given as an fp32 tensor, and then be added to with `accumulate`."""
+    import torch
+    m = _pkg()
+    p = _ce_struct(hidden, weight, targets, logit_scale, ignore_index)
+    if row_scale is not None:
+        _out(row_scale, "row_scale", (p.tokens,), (torch.float32,), hidden.device)
+        p.row_scale = row_scale.data_ptr()
+    if accumulate and (d_weight is None or d_weight.dtype != torch.float32):
+        raise ValueError("accumulate needs an fp32 d_weight")
+    with _on(stream):
+        dev = hidden.device
+        loss = _out(loss, "loss", (p.tokens,), (torch.float32,), dev)
+        lse = _out(lse, "lse", (p.tokens,), (torch.float32,), dev)
+        d_hidden = _out(d_hidden, "d_hidden", hidden.shape, (hidden.dtype,), dev)
+        d_weight = _out(d_weight, "d_weight", weight.shape, (hidden.dtype, torch.float32), dev)
+        p.loss, p.lse, p.d_hidden, p.d_weight = (x.data_ptr() for x in (loss, lse, d_hidden, d_weight))
+        p.d_weight_dtype = _dtypes()[d_weight.dtype]
+        p.accumulate = int(bool(accumulate))
+        lib = m.load_library()
+        at = ctypes.addressof(p)
+        ws = workspace
+        if ws is None:
+            ws = _workspace(None, lib.muon_linear_ce_workspace(at, 1, int(budget_bytes)), "muon_linear_ce_grad", dev)
+        m._check(lib.muon_linear_ce_grad(at, ws.data_ptr(), ws.numel(), m._stream(stream)), "muon_linear_ce_grad")
+    return loss, lse, d_hidden, d_weight
+
+
+def muon_expert_matmul(x, weight, offsets, transpose: bool = False, out=None, workspace=None, stream=None):
+    """y[t] = weight[e] x[t] (or weight[e]^T x[t] with `transpose`, the input
+    gradient) for the rows t in [offsets[e], offsets[e + 1]) of expert e.
+    x: (tokens, cols) (or (tokens, rows)); weight: (experts, rows, cols)
+    contiguous; both bf16 or both fp16.  Rows of no expert become zeros."""
+    import torch
+    m = _pkg()
+    dts = _dtypes()
+    half = (torch.bfloat16, torch.float16)
+    ld = _rows(x, "x", half)
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 3:
+        raise ValueError("weight must be a tensor of shape (experts, rows, cols)")
+    e, r, c = weight.shape
+    _out(weight, "weight", (e, r, c), (x.dtype,), x.device)
+    xc, yc = (r, c) if transpose else (c, r)
+    if x.shape[1] != xc:
+        raise ValueError(f"x must have {xc} columns, got {x.shape[1]}")
+    is64 = _index(offsets, "offsets", e + 1)
+    n = x.shape[0]
+    with _on(stream):
+        if out is None:
+            out, old = x.new_empty((n, yc)), yc
+        else:
+            old = _rows(out, "out", (x.dtype,), yc, n)
+        lib = m.load_library()
+        tr = int(bool(transpose))
+        ws = _workspace(workspace, lib.muon_expert_matmul_workspace(x.data_ptr(), ld, weight.data_ptr(), e, n, r, c, tr),
+                        "muon_expert_matmul", x.device)
+        m._check(lib.muon_expert_matmul(x.data_ptr(), ld, weight.data_ptr(), offsets.data_ptr(), is64, dts[x.dtype], e, n,
+                                        r, c, tr, out.data_ptr(), old, ws.data_ptr(), ws.numel(), m._stream(stream)),
+                 "muon_expert_matmul")
+    return out
+
+
+def muon_expert_wgrad(grad, x, offsets, out=None, out_dtype=None, accumulate: bool = False, workspace=None,
+                      stream=None):
+    """The experts' weight gradients, (experts, rows, cols): for each expert
+    the sum over its tokens of grad[t] x[t]^T.  grad: (tokens, rows), x:
+    (tokens, cols), both bf16 or both fp16.  `out_dtype`: theirs (default)
+    or fp32; `accumulate` adds to an fp32 `out`."""
+    import torch
+    m = _pkg()
+    dts = _dtypes()
+    half = (torch.bfloat16, torch.float16)
+    gld = _rows(grad, "grad", half)
+    n, r = grad.shape
+    xld = _rows(x, "x", (grad.dtype,), None, n)
+    c = x.shape[1]
+    is64 = _index(offsets, "offsets")
+    e = offsets.numel() - 1
+    if accumulate and (out is None or out.dtype != torch.float32):
+        raise ValueError("accumulate needs an fp32 out")
+    with _on(stream):
+        if out is None and out_dtype is not None:
+            out = torch.empty((e, r, c), dtype=out_dtype, device=x.device)
+        out = _out(out, "out", (e, r, c), (grad.dtype, torch.float32), x.device)
+        lib = m.load_library()
+        ws = _workspace(workspace, lib.muon_expert_wgrad_workspace(grad.data_ptr(), gld, x.data_ptr(), xld, e, n, r, c),
+                        "muon_expert_wgrad", x.device)
+        m._check(lib.muon_expert_wgrad(grad.data_ptr(), gld, x.data_ptr(), xld, offsets.data_ptr(), is64,
+                                       dts[grad.dtype], e, n, r, c, out.data_ptr(), dts[out.dtype],
+                                       int(bool(accumulate)), ws.data_ptr(), ws.numel(), m._stream(stream)),
+                 "muon_expert_wgrad")
+    return out
