@@ -70,17 +70,31 @@ cudaError_t launch_embed_grad(const EmbedGrad& a, void* workspace, int num_sms, 
 // with groups the ranges [offsets[e], offsets[e + 1]) of the token axis.
 enum { GROUP_NONE = 0, GROUP_M = 1, GROUP_K = 2 };
 
+// Softmax sums of the product's rows, one pair per row and 256-column tile:
+// (top, sum over the tile of exp2(x - top)), x = scale2 * product, without
+// the row's target column.  The product itself is stored when `store` is set.
+struct CeEpilogue {
+    float2* sums;         // [column tile][M]; null: no softmax
+    const void* targets;
+    int32_t targets64;
+    int32_t store;
+    float scale2;         // log2(e) * logit_scale
+};
+
 struct TrainGemm {
     const void* A;
     const void* B;
     void* C;
     int64_t lda, ldb, ldc;  // elements
     int64_t M, N, K;
-    int64_t b_stride, c_stride;  // elements, between groups
+    int64_t b_stride, c_stride;  // elements, between groups (c_stride: or splits)
     const void* offsets;
+    void* group_maps;        // GROUP_K: train_gemm_group_bytes of the workspace, 64-byte aligned
     const float* alpha_dev;  // multiplies alpha when not null
     int* status;
+    CeEpilogue ce;
     int64_t groups;
+    int32_t splits;      // GROUP_NONE: pieces of K, piece s into C + s * c_stride
     int32_t offsets64;
     int32_t group;
     int32_t dtype;       // of A and B
@@ -88,31 +102,51 @@ struct TrainGemm {
     int32_t accumulate;  // C += (fp32 only)
     int32_t kind;        // muon_kernel_kind_t of the launch
     bool a_mn, b_mn;
+    bool a_padded, b_padded;  // MN-major rows may be read up to a multiple of 64
     float alpha;
 };
 cudaError_t train_gemm(const TrainGemm& g, int num_sms, cudaStream_t st);
+size_t train_gemm_group_bytes(int64_t groups);
+int64_t train_gemm_col_tiles(int64_t N);           // 256-column tiles
+int64_t train_gemm_tiles(int64_t M, int64_t N);    // tiles of a plain product, one per CTA or CTA pair
+// out = alpha * the sum of `splits` fp32 matrices, in order.
+cudaError_t launch_split_sum(const float* parts, int64_t ld, int64_t stride, int splits, float alpha,
+                             const float* alpha_dev, void* out, int64_t out_ld, int out_dtype, int64_t rows,
+                             int64_t cols, int kind, int num_sms, cudaStream_t st);
 
 // Copies rows of 2-byte elements to rows of another pitch.
 cudaError_t launch_pack(const void* src, int64_t src_ld, void* dst, int64_t dst_ld, int64_t rows, int64_t cols,
                         int num_sms, cudaStream_t st);
 
 // ---- cross entropy rows (cross_entropy.cu) ---------------------------------
-struct CeRows {
+// A block of tokens; the arrays are the block's.
+struct CeBlock {
+    const void* hidden;      // the caller's rows
+    const void* weight;      // the caller's rows
     const void* targets;
     const float* row_scale;  // may be null
+    const float* scale_max;  // device: largest |row_scale|
+    const float2* sums;      // [column tile][tokens], see CeEpilogue
+    float* z_target;         // logit_scale * the target's logit
+    float* lse2;             // the normaliser in base 2
     float* loss;
     float* lse;
-    float* Z;          // block of logits, fp32, turned in place into the gradient's 16-bit rows
-    void* hidden;      // packed hidden rows of the block; ignored rows are cleared
-    const float* scale_max;  // device: largest |row_scale|
+    float* Z;                // logits; turned in place into the gradient's 16-bit rows
+    void* packed;            // copy of the hidden rows (null: none); ignored rows are cleared by ce_grad_rows
     int* status;
-    int64_t z_ld, hidden_ld;
-    int64_t tokens, vocab, dim, ignore_index;
-    int32_t targets64, dtype, with_grad;
+    int64_t hidden_ld, weight_ld, packed_ld, z_ld;
+    int64_t tokens, vocab, dim, ignore_index, col_tiles;
+    int32_t targets64, dtype;
     float logit_scale;
 };
-cudaError_t launch_ce_rows(const CeRows& r, cudaStream_t st);
-// out[0] = largest |row_scale| (1 when null), out[1] = out[0] * mult.
+// The targets' logits in fp32, and the packed copy.
+cudaError_t launch_ce_prepare(const CeBlock& b, int num_sms, cudaStream_t st);
+// Loss and normaliser from the tiles' sums.
+cudaError_t launch_ce_finish(const CeBlock& b, cudaStream_t st);
+// Logits -> their gradient.
+cudaError_t launch_ce_grad_rows(const CeBlock& b, cudaStream_t st);
+// out[0] = largest |row_scale| (1 when null), out[1] = out[0] * mult; clears
+// the status word.
 cudaError_t launch_ce_scale(const float* row_scale, int64_t tokens, float mult, float* out, int* status,
                             cudaStream_t st);
 // The fixed factor that keeps small fp16 logit gradients out of the

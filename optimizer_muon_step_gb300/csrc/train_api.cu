@@ -174,34 +174,71 @@ namespace {
 
 // Workspace: header and scalars, the packed weight (when its rows are not
 // 16-byte), the fp32 sums of d_weight (several blocks and a 16-bit result),
-// then per token of a block: the packed hidden row and the row of logits.
+// then for a block of tokens: the column tiles' softmax sums, the target
+// logits and normalisers, the packed hidden rows, and with gradients the rows
+// of logits and the pieces of d_hidden.
 struct CeLayout {
     int64_t block = 0;   // tokens per block
-    int64_t z_ld = 0, h_ld = 0, w_ld = 0;
-    bool pack_w = false, sums = false;
-    size_t w_off = 0, sum_off = 0, h_off = 0, z_off = 0, total = 0;
+    int64_t z_ld = 0, h_ld = 0, w_ld = 0, part_ld = 0;
+    int64_t col_tiles = 0;
+    int splits = 1;      // pieces of the vocabulary in d_hidden's product
+    bool pack_w = false, pack_h = false, sums = false;
+    size_t w_off = 0, sum_off = 0, tile_off = 0, zt_off = 0, lse_off = 0, h_off = 0, z_off = 0, part_off = 0, total = 0;
 };
 
 constexpr size_t kScalarsOff = 256;
 constexpr size_t kFixedBytes = 512;
+constexpr int kSms = 152;  // workspace sizes must not depend on the current device
+
+int64_t pitch64(int64_t cols) { return round_up(cols, 64); }
+
+// Pieces of the vocabulary that d_hidden's product (m x d, K = v) is cut into:
+// the product has few tiles and a long K, so whole tiles leave most of a last
+// wave of CTAs idle.  Cost in units of one 64-deep k-block of a tile
+// (0.35 us): waves * (blocks per piece + a tile's fill and drain), plus the
+// pieces' way through memory.
+int hidden_splits(int64_t m, int64_t d, int64_t v) {
+    const int64_t tiles = train_gemm_tiles(m, d), workers = m > 128 ? kSms / 2 : kSms, kb = (v + 63) / 64;
+    int best = 1;
+    double best_cost = 0;
+    for (int s = 1; s <= 64 && s * 8 <= kb; ++s) {
+        const double waves = static_cast<double>((tiles * s + workers - 1) / workers);
+        const double pieces = s > 1 ? 8.0 * s * m * d / 5e12 / 0.35e-6 + 8 : 0;
+        const double cost = waves * (static_cast<double>((kb + s - 1) / s) + 10) + pieces;
+        if (s == 1 || cost < best_cost) {
+            best = s;
+            best_cost = cost;
+        }
+    }
+    return best;
+}
 
 size_t ce_total(const muon_linear_ce_t* p, bool grad, int64_t block, CeLayout* L) {
     const int64_t v = p->vocab, d = p->dim;
+    auto take = [](size_t& at, int64_t bytes) {
+        const size_t o = at;
+        at += static_cast<size_t>(round_up(bytes, 256));
+        return o;
+    };
     L->block = block;
-    L->z_ld = round_up(v, 64);
-    L->h_ld = pitch8(d);
+    L->z_ld = pitch64(v);
+    L->h_ld = pitch64(d);
+    L->part_ld = round_up(d, 4);
+    L->col_tiles = train_gemm_col_tiles(v);
     L->pack_w = !tma_ready(p->weight, p->weight_ld);
-    L->w_ld = L->pack_w ? pitch8(d) : p->weight_ld;
+    L->pack_h = grad || !tma_ready(p->hidden, p->hidden_ld);
+    L->w_ld = L->pack_w ? pitch64(d) : p->weight_ld;
     L->sums = grad && block < p->tokens && p->d_weight_dtype != MUON_F32;
+    L->splits = grad ? hidden_splits(block, d, v) : 1;
     size_t at = kFixedBytes;
-    L->w_off = at;
-    if (L->pack_w) at += packed_bytes(v, d);
-    L->sum_off = at;
-    if (L->sums) at += static_cast<size_t>(round_up(4 * v * d, 256));
-    L->h_off = at;
-    at += packed_bytes(block, d);
-    L->z_off = at;
-    at += static_cast<size_t>(4 * block * L->z_ld);
+    L->w_off = take(at, L->pack_w ? 2 * v * L->w_ld : 0);
+    L->sum_off = take(at, L->sums ? 4 * v * d : 0);
+    L->tile_off = take(at, 8 * block * L->col_tiles);
+    L->zt_off = take(at, 4 * block);
+    L->lse_off = take(at, 4 * block);
+    L->h_off = take(at, L->pack_h ? 2 * block * L->h_ld : 0);
+    L->z_off = take(at, grad ? 4 * block * L->z_ld : 0);
+    L->part_off = take(at, L->splits > 1 ? 4 * L->splits * block * L->part_ld : 0);
     L->total = at;
     return at;
 }
@@ -285,17 +322,40 @@ muon_status_t ce_run(const muon_linear_ce_t* p, bool grad, void* workspace, size
     }
     for (int64_t t0 = 0; t0 < n && e == cudaSuccess; t0 += block) {
         const int64_t m = std::min(block, n - t0);
-        const uint8_t* hidden = static_cast<const uint8_t*>(p->hidden) + 2 * t0 * p->hidden_ld;
-        float* Z = reinterpret_cast<float*>(ws + L.z_off);
-        void* H = ws + L.h_off;
-        e = launch_pack(hidden, p->hidden_ld, H, L.h_ld, m, d, num_sms, st);
+        CeBlock c = {};
+        c.hidden = static_cast<const uint8_t*>(p->hidden) + 2 * t0 * p->hidden_ld;
+        c.hidden_ld = p->hidden_ld;
+        c.weight = p->weight;
+        c.weight_ld = p->weight_ld;
+        c.targets = static_cast<const uint8_t*>(p->targets) + t0 * ie;
+        c.row_scale = grad && p->row_scale ? p->row_scale + t0 : nullptr;
+        c.scale_max = scalars;
+        c.sums = reinterpret_cast<const float2*>(ws + L.tile_off);
+        c.z_target = reinterpret_cast<float*>(ws + L.zt_off);
+        c.lse2 = reinterpret_cast<float*>(ws + L.lse_off);
+        c.loss = p->loss + t0;
+        c.lse = p->lse + t0;
+        c.Z = reinterpret_cast<float*>(ws + L.z_off);
+        c.z_ld = L.z_ld;
+        c.packed = L.pack_h ? ws + L.h_off : nullptr;
+        c.packed_ld = L.h_ld;
+        c.status = status;
+        c.tokens = m;
+        c.vocab = v;
+        c.dim = d;
+        c.ignore_index = p->ignore_index;
+        c.col_tiles = L.col_tiles;
+        c.targets64 = p->targets_dtype == MUON_I64;
+        c.dtype = p->dtype;
+        c.logit_scale = p->logit_scale;
+        e = launch_ce_prepare(c, num_sms, st);
         if (e != cudaSuccess) break;
         TrainGemm g = {};
-        g.A = H;
-        g.lda = L.h_ld;
+        g.A = L.pack_h ? c.packed : c.hidden;
+        g.lda = L.pack_h ? L.h_ld : p->hidden_ld;
         g.B = weight;
         g.ldb = L.w_ld;
-        g.C = Z;
+        g.C = grad ? c.Z : nullptr;
         g.ldc = L.z_ld;
         g.c_dtype = MUON_F32;
         g.M = m;
@@ -303,57 +363,56 @@ muon_status_t ce_run(const muon_linear_ce_t* p, bool grad, void* workspace, size
         g.K = d;
         g.alpha = 1.f;
         g.dtype = p->dtype;
+        g.status = status;
+        g.ce.sums = reinterpret_cast<float2*>(ws + L.tile_off);
+        g.ce.targets = c.targets;
+        g.ce.targets64 = c.targets64;
+        g.ce.store = grad;
+        g.ce.scale2 = p->logit_scale * 1.4426950408889634f;
         g.kind = MUON_KERNEL_CE_LOGITS;
         e = train_gemm(g, num_sms, st);
-        if (e != cudaSuccess) break;
-        CeRows r = {};
-        r.targets = static_cast<const uint8_t*>(p->targets) + t0 * ie;
-        r.row_scale = grad && p->row_scale ? p->row_scale + t0 : nullptr;
-        r.loss = p->loss + t0;
-        r.lse = p->lse + t0;
-        r.Z = Z;
-        r.z_ld = L.z_ld;
-        r.hidden = H;
-        r.hidden_ld = L.h_ld;
-        r.scale_max = scalars;
-        r.status = status;
-        r.tokens = m;
-        r.vocab = v;
-        r.dim = d;
-        r.ignore_index = p->ignore_index;
-        r.targets64 = p->targets_dtype == MUON_I64;
-        r.dtype = p->dtype;
-        r.with_grad = grad;
-        r.logit_scale = p->logit_scale;
-        e = launch_ce_rows(r, st);
+        if (e == cudaSuccess) e = launch_ce_finish(c, st);
         if (e != cudaSuccess || !grad) continue;
+        e = launch_ce_grad_rows(c, st);
+        if (e != cudaSuccess) break;
         // d_hidden = G W; the rows of G lie in the front halves of Z's rows
+        const int splits = m == L.block ? L.splits
+                                        : std::min<int>(hidden_splits(m, d, v), static_cast<int>(L.splits * L.block / m));
+        void* dh = static_cast<uint8_t*>(p->d_hidden) + 2 * t0 * d;
+        float* parts = reinterpret_cast<float*>(ws + L.part_off);
         g = TrainGemm{};
-        g.A = Z;
+        g.A = c.Z;
         g.lda = 2 * L.z_ld;
         g.B = weight;
         g.ldb = L.w_ld;
         g.b_mn = true;
-        g.C = static_cast<uint8_t*>(p->d_hidden) + 2 * t0 * d;
-        g.ldc = d;
-        g.c_dtype = p->dtype;
+        g.b_padded = L.pack_w;
+        g.splits = splits;
+        g.C = splits > 1 ? static_cast<void*>(parts) : dh;
+        g.ldc = splits > 1 ? L.part_ld : d;
+        g.c_stride = m * L.part_ld;
+        g.c_dtype = splits > 1 ? static_cast<int32_t>(MUON_F32) : p->dtype;
         g.M = m;
         g.N = d;
         g.K = v;
         g.alpha = 1.f;
-        g.alpha_dev = scalars + 1;
+        g.alpha_dev = splits > 1 ? nullptr : scalars + 1;
         g.dtype = p->dtype;
+        g.status = status;
         g.kind = MUON_KERNEL_CE_GRAD;
         e = train_gemm(g, num_sms, st);
+        if (e == cudaSuccess && splits > 1)
+            e = launch_split_sum(parts, L.part_ld, g.c_stride, splits, 1.f, scalars + 1, dh, d, p->dtype, m, d,
+                                 MUON_KERNEL_CE_GRAD, num_sms, st);
         if (e != cudaSuccess) break;
         // d_weight += G^T H
         g = TrainGemm{};
-        g.A = Z;
+        g.A = c.Z;
         g.lda = 2 * L.z_ld;
-        g.a_mn = true;
-        g.B = H;
+        g.a_mn = g.a_padded = true;
+        g.B = c.packed;
         g.ldb = L.h_ld;
-        g.b_mn = true;
+        g.b_mn = g.b_padded = true;
         g.C = L.sums ? static_cast<void*>(ws + L.sum_off) : p->d_weight;
         g.ldc = d;
         g.c_dtype = L.sums ? static_cast<int32_t>(MUON_F32) : p->d_weight_dtype;
@@ -364,6 +423,7 @@ muon_status_t ce_run(const muon_linear_ce_t* p, bool grad, void* workspace, size
         g.alpha = 1.f;
         g.alpha_dev = scalars + 1;
         g.dtype = p->dtype;
+        g.status = status;
         g.kind = MUON_KERNEL_CE_GRAD;
         e = train_gemm(g, num_sms, st);
     }
@@ -493,7 +553,7 @@ size_t muon_expert_wgrad_workspace(const void* grad, int64_t grad_ld, const void
     size_t n = kHeaderBytes;
     if (!tma_ready(grad, grad_ld)) n += packed_bytes(tokens, rows);
     if (!tma_ready(x, x_ld)) n += packed_bytes(tokens, cols);
-    return n;
+    return n + static_cast<size_t>(round_up(static_cast<int64_t>(train_gemm_group_bytes(experts)), 256));
 }
 
 muon_status_t muon_expert_wgrad(const void* grad, int64_t grad_ld, const void* x, int64_t x_ld, const void* offsets,
@@ -533,6 +593,8 @@ muon_status_t muon_expert_wgrad(const void* grad, int64_t grad_ld, const void* x
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     uint8_t* at = ws + kHeaderBytes;
     TrainGemm g = {};
+    g.group_maps = at;
+    at += round_up(static_cast<int64_t>(train_gemm_group_bytes(experts)), 256);
     g.A = grad;
     g.lda = grad_ld;
     g.B = x;

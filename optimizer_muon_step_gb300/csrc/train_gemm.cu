@@ -1,96 +1,608 @@
-// Matrix products of the head and the experts: C = alpha * A B with 16-bit
-// operands and fp32 sums, plain or grouped by expert.
+// Matrix products of the head and the experts on Blackwell tensor cores
+// (sm_103a): C = alpha * A B with 16-bit operands and fp32 sums, plain or
+// grouped by expert.
+//
+//   GROUP_NONE  C = A B, K optionally split into pieces of their own output
+//   GROUP_M     rows [o_e, o_{e+1}) of A and C use B_e
+//   GROUP_K     C_e = sum over k in [o_e, o_{e+1})
+//
+// One persistent kernel of 6 warps per CTA (or CTA pair), with the roles of
+// the Newton-Schulz kernel: warp 0 feeds a shared-memory ring by TMA, warp 1
+// issues tcgen05.mma into two 256-column TMEM accumulators, warps 2..5 empty
+// the other accumulator.  Either operand may be K-major or MN-major (the
+// instruction descriptor's major bits), so gradients of the weights and the
+// inputs need no transposed copy.
+//
+// The groups' ranges are read from the device, so a call needs no host
+// synchronisation.  Each role finds its tiles by itself: the warp holds 32
+// groups' ranges at a time, one per lane, and walks the tile list in order.
+// GROUP_M tiles that reach past their group load the neighbour's rows and
+// store only their own.  GROUP_K must not see the neighbour's rows at all (0
+// times NaN is NaN): each group reads through its own copy of the tensor
+// maps whose row extent ends where the group does, so the TMA unit fills the
+// rest of the last k-block with zeros.
+//
+// The softmax epilogue (CE) reduces each row of a logits tile to its maximum
+// and sum of exponentials straight from TMEM; the logits are stored only
+// when their gradient is wanted.
+#include <string.h>
+
+#include "host_checks.h"
+#include "tcgen05.h"
 #include "train.h"
 
 namespace muon {
 namespace {
 
-constexpr int TS = 64;  // tile rows and columns
-constexpr int TK = 16;
+constexpr int BM = 128;   // rows of a CTA's tile
+constexpr int BN = 256;   // columns of a tile
+constexpr int BK = 64;    // one 128-byte swizzle row of 16-bit elements
+constexpr int A_BYTES = BM * BK * 2;
+constexpr int EPI_WARPS = 4;
+constexpr int NUM_THREADS = 64 + 32 * EPI_WARPS;
+constexpr int TMEM_COLS = 512;
+constexpr int EBUF_BYTES = 32 * 128;  // a block of 32 rows x 128 bytes on its way out
+constexpr int NSLOT = 2;              // blocks per epilogue warp
+constexpr int EBUFS_BYTES = EPI_WARPS * NSLOT * EBUF_BYTES;
 
-__device__ __forceinline__ int64_t clamped_offset(const TrainGemm& g, int64_t e) {
-    const int64_t n = g.group == GROUP_M ? g.M : g.K;
-    const int64_t o = load_index(g.offsets, g.offsets64, e);
-    return o < 0 ? 0 : o > n ? n : o;
+// Ring: pairs stage 128 rows of each operand per CTA, two k-blocks per
+// stage; single CTAs 128 and 256 rows, one k-block per stage.
+template <bool kPair>
+struct Ring {
+    static constexpr int B_ROWS = kPair ? BN / 2 : BN;
+    static constexpr int SUB_BYTES = A_BYTES + B_ROWS * BK * 2;
+    static constexpr int KPS = kPair ? 2 : 1;
+    static constexpr int STAGES = kPair ? 3 : 4;
+    static constexpr int STAGE_BYTES = KPS * SUB_BYTES;
+    static constexpr int TILE_M = kPair ? 2 * BM : BM;
+    static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EBUFS_BYTES + 512;
+};
+
+struct GemmParams {
+    CUtensorMap tm_a, tm_b, tm_c;
+    const CUtensorMap* group_maps;  // GROUP_K: A's and B's map of each group
+    const void* offsets;
+    void* C;
+    const float* alpha_dev;
+    int* status;
+    CeEpilogue ce;
+    int64_t ldc, c_stride;          // elements
+    int32_t M, N, K;                // GROUP_M: M rows in all; GROUP_K: K rows in all
+    int32_t tiles_m, tiles_n, total_tiles;  // GROUP_M: tiles_m and total_tiles are found on the device
+    int32_t band;                   // rows of tiles walked together (GROUP_NONE, GROUP_K)
+    int32_t groups, group, offsets64;
+    int32_t k_blocks;               // per split (GROUP_NONE)
+    int32_t c_dtype, accumulate, tma_c;
+    int32_t chunked_a, chunked_b;   // MN-major maps are 4-D, two or four 64-row chunks a copy
+    uint32_t idesc;                 // without M and N
+    bool a_mn, b_mn;
+    float alpha;
+};
+
+struct Tile {
+    int row0, rows_end;  // first row of the (pair) tile, end of its rows
+    int col0;
+    int c2;              // third coordinate of C: group or split
+    int group;           // weight matrix (GROUP_M), tensor maps (GROUP_K)
+    int k0;              // first k (elements)
+    int nk;              // k-blocks
+};
+
+__device__ __forceinline__ int clamped(const GemmParams& p, int e, int n) {
+    const int64_t o = load_index(p.offsets, p.offsets64, e);
+    return o < 0 ? 0 : o > n ? n : static_cast<int>(o);
 }
 
-// Range [lo, hi) of group e.  GROUP_M has two more, e = -1 and e = groups:
-// the rows before the first and after the last, whose products are zeros.
-__device__ __forceinline__ void group_range(const TrainGemm& g, int64_t e, int64_t* lo, int64_t* hi) {
-    *lo = e < 0 ? 0 : clamped_offset(g, e);
-    *hi = e >= g.groups ? g.M : clamped_offset(g, e + 1);
-    if (*hi < *lo) *hi = *lo;
-}
+// Walks the tile list; every lane of a warp calls next() together.
+template <int TILE_M>
+struct Walker {
+    const GemmParams& p;
+    int lane;
+    // GROUP_M: the window of groups base - 1 .. base + 30 (lane l holds group
+    // base + l - 1; -1 and `groups` are the rows before and after all groups)
+    int base, first, total, lo, hi, incl;
 
-template <int DT>
-__device__ __forceinline__ float ld(const void* p, int64_t i) {
-    return Elem<DT>::load(static_cast<const typename Elem<DT>::T*>(p)[i]);
-}
+    __device__ Walker(const GemmParams& prm, int ln) : p(prm), lane(ln), base(-32), first(0), total(0), lo(0), hi(0), incl(0) {}
 
-template <int DT>
-__global__ void __launch_bounds__(256) gemm_kernel(const TrainGemm g) {
-    __shared__ float sa[TK][TS + 1], sb[TK][TS + 1];
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && g.status) *g.status = 0;
-    int64_t row0 = static_cast<int64_t>(blockIdx.y) * TS, rows_end = g.M, k_lo = 0, k_hi = g.K;
-    int64_t b_off = 0, c_off = 0;
-    if (g.group == GROUP_M) {
-        int64_t tile = blockIdx.y, e = -1, lo = 0, hi = 0;
-        for (; e <= g.groups; ++e) {
-            group_range(g, e, &lo, &hi);
-            const int64_t n = (hi - lo + TS - 1) / TS;
-            if (tile < n) break;
-            tile -= n;
-        }
-        if (e > g.groups) return;
-        row0 = lo + tile * TS;
-        rows_end = hi;
-        if (e < 0 || e == g.groups) k_hi = 0;
-        else b_off = e * g.b_stride;
-    } else if (g.group == GROUP_K) {
-        const int64_t tm = (g.M + TS - 1) / TS;
-        const int64_t e = blockIdx.y / tm;
-        row0 = (blockIdx.y - e * tm) * TS;
-        group_range(g, e, &k_lo, &k_hi);
-        c_off = e * g.c_stride;
-    }
-    const int64_t col0 = static_cast<int64_t>(blockIdx.x) * TS;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[4][4] = {};
-    for (int64_t k0 = k_lo; k0 < k_hi; k0 += TK) {
-        for (int i = threadIdx.x; i < TS * TK; i += 256) {
-            const int ka = g.a_mn ? i / TS : i % TK, ma = g.a_mn ? i % TS : i / TK;
-            const int kb = g.b_mn ? i / TS : i % TK, nb = g.b_mn ? i % TS : i / TK;
-            const int64_t m = row0 + ma, n = col0 + nb;
-            sa[ka][ma] = m < rows_end && k0 + ka < k_hi
-                             ? ld<DT>(g.A, g.a_mn ? (k0 + ka) * g.lda + m : m * g.lda + k0 + ka) : 0.f;
-            sb[kb][nb] = n < g.N && k0 + kb < k_hi
-                             ? ld<DT>(g.B, b_off + (g.b_mn ? (k0 + kb) * g.ldb + n : n * g.ldb + k0 + kb)) : 0.f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < TK; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] += sa[k][ty * 4 + i] * sb[k][tx * 4 + j];
-        __syncthreads();
-    }
-    const float alpha = g.alpha_dev ? g.alpha * *g.alpha_dev : g.alpha;
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int64_t m = row0 + ty * 4 + i, n = col0 + tx * 4 + j;
-            if (m >= rows_end || n >= g.N) continue;
-            const int64_t at = c_off + m * g.ldc + n;
-            const float v = alpha * acc[i][j];
-            if (g.c_dtype == MUON_F32) {
-                float* c = static_cast<float*>(g.C) + at;
-                *c = g.accumulate ? *c + v : v;
-            } else if (g.c_dtype == MUON_BF16) {
-                static_cast<__nv_bfloat16*>(g.C)[at] = __float2bfloat16_rn(v);
+    __device__ bool next(int t, Tile& o) {
+        if (p.group != GROUP_M) {
+            if (t >= p.total_tiles) return false;
+            const int per = p.tiles_m * p.tiles_n;
+            const int s = t / per;
+            const int r = t - s * per;
+            const int span = p.band * p.tiles_n;
+            const int b = r / span;
+            const int rr = r - b * span;
+            const int left = p.tiles_m - b * p.band;
+            const int h = left < p.band ? left : p.band;
+            const int n = rr / h;
+            o.row0 = (b * p.band + rr - n * h) * TILE_M;
+            o.rows_end = p.M;
+            o.col0 = n * BN;
+            o.c2 = o.group = s;
+            if (p.group == GROUP_K) {
+                const int a = clamped(p, s, p.K), e = clamped(p, s + 1, p.K);
+                o.k0 = a;
+                o.nk = e > a ? (e - a + BK - 1) / BK : 0;
             } else {
-                static_cast<__half*>(g.C)[at] = __float2half_rn(v);
+                const int all = (p.K + BK - 1) / BK;
+                const int kb = s * p.k_blocks;
+                o.k0 = kb * BK;
+                const int left_k = all - kb;  // the last pieces may be empty
+                o.nk = left_k <= 0 ? 0 : left_k < p.k_blocks ? left_k : p.k_blocks;
+            }
+            return true;
+        }
+        while (t >= first + total) {
+            first += total;
+            base += 32;
+            if (base > p.groups + 1) return false;
+            const int e = base + lane - 1;
+            lo = hi = 0;
+            if (e <= p.groups) {
+                lo = e < 0 ? 0 : clamped(p, e, p.M);
+                hi = e >= p.groups ? p.M : clamped(p, e + 1, p.M);
+            }
+            incl = hi > lo ? (hi - lo + TILE_M - 1) / TILE_M * p.tiles_n : 0;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, incl, d);
+                if (lane >= d) incl += x;
+            }
+            total = __shfl_sync(0xffffffffu, incl, 31);
+        }
+        const int src = __ffs(__ballot_sync(0xffffffffu, t - first < incl)) - 1;
+        const int prev = __shfl_sync(0xffffffffu, incl, src > 0 ? src - 1 : 0);
+        const int a = __shfl_sync(0xffffffffu, lo, src), e = __shfl_sync(0xffffffffu, hi, src);
+        const int r = t - first - (src > 0 ? prev : 0);
+        const int tm = (e - a + TILE_M - 1) / TILE_M;
+        const int n = r / tm;
+        const int g = base + src - 1;
+        o.row0 = a + (r - n * tm) * TILE_M;
+        o.rows_end = e;
+        o.col0 = n * BN;
+        o.c2 = 0;
+        o.group = g;
+        o.k0 = 0;
+        o.nk = g < 0 || g >= p.groups ? 0 : (p.K + BK - 1) / BK;
+        return true;
+    }
+};
+
+// Columns the MMA computes: 256, or at the edge the next multiple of 32 (16
+// for single CTAs; of 128 with chunked pairs, whose halves start on a chunk).
+template <bool kPair>
+__device__ __forceinline__ int tile_cols(const GemmParams& p, int col0) {
+    const int rem = p.N - col0;
+    const int q = !kPair ? 15 : p.b_mn && p.chunked_b ? 127 : 31;
+    return rem < BN ? (rem + q) & ~q : BN;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, int dtype) {
+    if (dtype == MUON_BF16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// The finished block in shared memory (32 rows of 128 bytes, swizzled) to C
+// with plain stores: rows of a group that ends inside the block, and C's that
+// no tensor map can describe.
+__device__ __forceinline__ void store_rows(const GemmParams& p, const uint8_t* buf, int row, int rows_end, int col,
+                                           int c2, int lane) {
+    const bool wide = p.c_dtype == MUON_F32;
+    const int c = col + (wide ? lane : 2 * lane);
+    const int rows = rows_end - row < 32 ? rows_end - row : 32;
+    for (int r = 0; r < rows; ++r) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(buf + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+        const int64_t at = c2 * p.c_stride + static_cast<int64_t>(row + r) * p.ldc + c;
+        if (wide) {
+            if (c < p.N) {
+                float* d = static_cast<float*>(p.C) + at;
+                const float v = __uint_as_float(w);
+                *d = p.accumulate ? __fadd_rn(*d, v) : v;
+            }
+        } else {
+            uint16_t* d = static_cast<uint16_t*>(p.C) + at;
+            if (c + 1 < p.N && (reinterpret_cast<uintptr_t>(d) & 3) == 0) {
+                *reinterpret_cast<uint32_t*>(d) = w;
+            } else {
+                if (c < p.N) d[0] = static_cast<uint16_t>(w);
+                if (c + 1 < p.N) d[1] = static_cast<uint16_t>(w >> 16);
             }
         }
+    }
+}
+
+// Softmax sums of one row of a tile, base 2: after all columns, sum =
+// sum exp2(x - top), x = logit * log2(e) * logit_scale, the target's column
+// left out (its logit is computed apart, see cross_entropy.cu).
+struct RowSums {
+    float top, sum;
+    __device__ __forceinline__ void add(const float (&x)[32]) {
+        float m = x[0];
+#pragma unroll
+        for (int i = 1; i < 32; ++i) m = fmaxf(m, x[i]);
+        m = fmaxf(m, top);
+        // an infinite maximum is not subtracted: inf - inf would be NaN where
+        // the sum is inf, and -inf leaves the sum at 0
+        const float ref = isinf(m) ? 0.f : m;
+        float s = top == -INFINITY ? 0.f : sum * ex2((isinf(top) ? 0.f : top) - ref);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s += ex2(x[i] - ref);
+        top = m;
+        sum = s;
+    }
+};
+
+template <bool kPair, bool kCe>
+__device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
+    typedef Ring<kPair> R;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* ebufs = smem + R::STAGES * R::STAGE_BYTES;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(ebufs + EBUFS_BYTES);
+    uint64_t* full_bar = bars;
+    uint64_t* empty_bar = bars + R::STAGES;
+    uint64_t* tfull_bar = bars + 2 * R::STAGES;
+    uint64_t* tempty_bar = tfull_bar + 2;
+    uint64_t* drain_bar = tempty_bar + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int rank = kPair ? static_cast<int>(cluster_rank()) : 0;
+    const int worker = kPair ? blockIdx.x >> 1 : blockIdx.x;
+    const int workers = kPair ? gridDim.x >> 1 : gridDim.x;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < R::STAGES; ++s) {
+            mbar_init(smem_u32(&full_bar[s]), 1);
+            mbar_init(smem_u32(&empty_bar[s]), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(smem_u32(&tfull_bar[a]), 1);
+            mbar_init(smem_u32(&tempty_bar[a]), (kPair ? 2 : 1) * EPI_WARPS);
+        }
+        mbar_init(smem_u32(drain_bar), 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&p.tm_a);
+        tma_prefetch_desc(&p.tm_b);
+        if (p.tma_c) tma_prefetch_desc(&p.tm_c);
+    }
+    if (warp == 1) {
+        if (kPair) {
+            tmem_alloc_pair(smem_u32(tmem_slot), TMEM_COLS);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
+            tmem_relinquish();
+        }
+    }
+    tc_fence_before();
+    if (kPair) cluster_sync_all();
+    else __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    // the prologue above touched only shared memory, TMEM and parameters
+    pdl_wait_then_release();
+    // a GROUP_M product is a call's only kernel but for copies: it clears the
+    // status word, which a wait that runs out sets seconds later
+    if (p.group == GROUP_M && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
+
+    Walker<R::TILE_M> walk(p, lane);
+    Tile tile;
+    if (warp == 0) {
+        // ---------------- TMA producer ----------------
+        int stage = 0;
+        uint32_t phase = 0;
+        int last_parity[R::STAGES];
+        for (int s = 0; s < R::STAGES; ++s) last_parity[s] = -1;
+        bool ok = true;
+        int acquired = -1;  // GROUP_K: the group whose tensor maps this thread has acquired
+        for (int t = worker; ok && walk.next(t, tile); t += workers) {
+            if (lane == 0) {
+                const CUtensorMap* ma = &p.tm_a;
+                const CUtensorMap* mb = &p.tm_b;
+                if (p.group == GROUP_K) {
+                    ma = p.group_maps + 2 * tile.group;
+                    mb = ma + 1;
+                    if (acquired != tile.group && tile.nk > 0) {
+                        acquired = tile.group;
+                        asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(ma) : "memory");
+                        asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(mb) : "memory");
+                    }
+                }
+                const int row = tile.row0 + rank * BM;
+                const int b0 = tile.col0 + (kPair ? rank * (tile_cols<kPair>(p, tile.col0) / 2) : 0);
+                const int b2 = p.group == GROUP_M ? tile.group : 0;
+                for (int kb0 = 0; kb0 < tile.nk; kb0 += R::KPS) {
+                    if (!wait_bounded(smem_u32(&empty_bar[stage]), phase ^ 1u, abort_flag, p.status)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t fb = smem_u32(&full_bar[stage]);
+                    const uint32_t fl = kPair ? mapa_shared(fb, 0) : fb;
+                    const int nsub = tile.nk - kb0 < R::KPS ? tile.nk - kb0 : R::KPS;
+                    if (rank == 0) mbar_expect_tx(fb, (kPair ? 2 : 1) * R::SUB_BYTES * nsub);
+                    auto load3 = [&](uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2) {
+                        if (kPair) tma_load_3d_pair(dst, map, c0, c1, c2, fl);
+                        else tma_load_3d(dst, map, c0, c1, c2, fl);
+                    };
+                    auto load_mn = [&](uint32_t dst, const CUtensorMap* map, int chunked, int r0, int nchunks, int k, int c2) {
+                        if (chunked) {
+                            for (int c = 0; c < nchunks; c += 2) {
+                                const uint32_t d = dst + static_cast<uint32_t>(c) * MN_CHUNK_BYTES;
+                                if (kPair) tma_load_4d_pair(d, map, 0, k, (r0 >> 6) + c, c2, fl);
+                                else tma_load_4d(d, map, 0, k, (r0 >> 6) + c, c2, fl);
+                            }
+                        } else {
+                            for (int c = 0; c < nchunks; ++c)
+                                load3(dst + static_cast<uint32_t>(c) * MN_CHUNK_BYTES, map, r0 + 64 * c, k, c2);
+                        }
+                    };
+                    for (int q = 0; q < nsub; ++q) {
+                        const int k = tile.k0 + (kb0 + q) * BK;
+                        const uint32_t sa = smem_u32(smem + stage * R::STAGE_BYTES + q * R::SUB_BYTES);
+                        const uint32_t sb = sa + A_BYTES;
+                        if (p.a_mn) load_mn(sa, ma, p.chunked_a, row, BM / 64, k, 0);
+                        else load3(sa, ma, k, row, 0);
+                        if (p.b_mn) load_mn(sb, mb, p.chunked_b, b0, R::B_ROWS / 64, k, b2);
+                        else load3(sb, mb, k, b0, b2);
+                    }
+                    last_parity[stage] = static_cast<int>(phase);
+                    if (++stage == R::STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        }
+        // drain: every issued copy must land before the CTA may exit (the even
+        // CTA's full barriers count both CTAs' copies)
+        if (lane == 0 && rank == 0)
+            for (int s = 0; s < R::STAGES; ++s)
+                if (last_parity[s] >= 0) wait_drain(smem_u32(&full_bar[s]), static_cast<uint32_t>(last_parity[s]));
+        __syncwarp();
+    } else if (warp == 1 && rank == 0) {
+        // ---------------- MMA issuer ----------------
+        int stage = 0;
+        uint32_t phase = 0;
+        int local = 0;
+        bool ok = true;
+        for (int t = worker; ok && walk.next(t, tile); t += workers) {
+            if (tile.nk == 0) continue;
+            if (lane == 0) {
+                const int acc = local & 1;
+                const uint32_t acc_phase = static_cast<uint32_t>(local >> 1) & 1u;
+                ok = wait_bounded(smem_u32(&tempty_bar[acc]), acc_phase ^ 1u, abort_flag, p.status);
+                tc_fence_after();
+                const int n = tile_cols<kPair>(p, tile.col0);
+                const uint32_t idesc = p.idesc | (static_cast<uint32_t>(n >> 3) << 17) |
+                                       (static_cast<uint32_t>(R::TILE_M >> 4) << 24);
+                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
+                for (int kb0 = 0; ok && kb0 < tile.nk; kb0 += R::KPS) {
+                    if (!wait_bounded(smem_u32(&full_bar[stage]), phase, abort_flag, p.status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const int nsub = tile.nk - kb0 < R::KPS ? tile.nk - kb0 : R::KPS;
+                    for (int q = 0; q < nsub; ++q) {
+                        const uint32_t sa = smem_u32(smem + stage * R::STAGE_BYTES + q * R::SUB_BYTES);
+                        const uint32_t sb = sa + A_BYTES;
+#pragma unroll
+                        for (int k = 0; k < BK / 16; ++k) {
+                            const uint64_t da = operand_desc(sa, k, p.a_mn), db = operand_desc(sb, k, p.b_mn);
+                            const uint32_t more = (kb0 | q | k) != 0 ? 1u : 0u;
+                            if (kPair) tc_mma_pair(d_tmem, da, db, idesc, more);
+                            else tc_mma(d_tmem, da, db, idesc, more);
+                        }
+                    }
+                    if (kPair) tc_commit_pair_mc(smem_u32(&empty_bar[stage]), 0x3);
+                    else tc_commit(smem_u32(&empty_bar[stage]));
+                    if (++stage == R::STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (ok) {
+                    if (kPair) tc_commit_pair_mc(smem_u32(&tfull_bar[acc]), 0x3);
+                    else tc_commit(smem_u32(&tfull_bar[acc]));
+                }
+            }
+            ++local;
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        }
+        // drain: all issued MMAs complete before TMEM is released
+        if (lane == 0) {
+            if (kPair) tc_commit_pair_mc(smem_u32(drain_bar), 0x1);
+            else tc_commit(smem_u32(drain_bar));
+            wait_drain(smem_u32(drain_bar), 0);
+        }
+        __syncwarp();
+    } else if (warp >= 2) {
+        // ---------------- epilogue ----------------
+        const int quarter = warp & 3;  // TMEM lanes 32 * quarter .. + 31
+        const int ew = warp - 2;
+        uint8_t* slots = ebufs + NSLOT * ew * EBUF_BYTES;
+        uint32_t seq = 0;  // blocks this warp has written; block n uses slot n % NSLOT and commits one bulk group
+        int local = 0;
+        const float alpha = p.alpha_dev ? p.alpha * *p.alpha_dev : p.alpha;
+        const int cols = p.c_dtype == MUON_F32 ? 32 : 64;
+        for (int t = worker; walk.next(t, tile); t += workers) {
+            const int acc = local & 1;
+            const uint32_t acc_phase = static_cast<uint32_t>(local >> 1) & 1u;
+            const int row = tile.row0 + rank * BM + quarter * 32;
+            const bool live = tile.nk > 0;
+            if (live) {
+                if (!wait_bounded(smem_u32(&tfull_bar[acc]), acc_phase, abort_flag, p.status)) break;
+                tc_fence_after();
+                ++local;
+            }
+            const uint32_t t_addr = tmem_base + static_cast<uint32_t>(acc * BN) + (static_cast<uint32_t>(quarter * 32) << 16);
+            // an empty group adds nothing
+            const bool mine = row < tile.rows_end && (live || !p.accumulate);
+            const bool by_tma = p.tma_c && (p.group != GROUP_M || row + 32 <= tile.rows_end);
+            RowSums rs = {-INFINITY, 0.f};
+            int target = -1;
+            if (kCe && mine && row + lane < p.M) {
+                const int64_t tg = load_index(p.ce.targets, p.ce.targets64, row + lane);
+                target = tg >= 0 && tg < p.N ? static_cast<int>(tg) : -1;
+            }
+            if (mine) {
+                for (int c = 0; c < BN; c += cols) {
+                    const int col = tile.col0 + c;
+                    if (col >= p.N) break;
+                    const uint32_t b = seq % NSLOT;
+                    uint8_t* buf = slots + b * EBUF_BYTES;
+                    const bool out = !kCe || p.ce.store;
+                    if (out) {
+                        if (lane == 0) bulk_wait_read<NSLOT - 1>();
+                        __syncwarp();
+                    }
+                    uint8_t* brow = buf + lane * 128;
+                    const int sw = lane & 7;
+                    for (int h = 0; h < cols; h += 32) {
+                        float v[32];
+                        if (live) {
+                            tmem_load_32cols(t_addr + static_cast<uint32_t>(c + h), v);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = 0.f;
+                        }
+                        if (kCe) {
+                            if (out) {
+#pragma unroll
+                                for (int q = 0; q < 8; ++q)
+                                    *reinterpret_cast<float4*>(brow + ((q ^ sw) << 4)) =
+                                        make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                            }
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] *= p.ce.scale2;
+                            const int off = target - col;
+                            if (__any_sync(0xffffffffu, off >= 0 && off < 32)) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (i == off) v[i] = -INFINITY;
+                            }
+                            if (col + 32 > p.N) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (col + i >= p.N) v[i] = -INFINITY;
+                            }
+                            rs.add(v);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] *= alpha;
+                            if (cols == 32) {
+#pragma unroll
+                                for (int q = 0; q < 8; ++q)
+                                    *reinterpret_cast<float4*>(brow + ((q ^ sw) << 4)) =
+                                        make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                            } else {
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    *reinterpret_cast<uint4*>(brow + (((h / 8 + q) ^ sw) << 4)) =
+                                        make_uint4(pack16(v[8 * q], v[8 * q + 1], p.c_dtype),
+                                                   pack16(v[8 * q + 2], v[8 * q + 3], p.c_dtype),
+                                                   pack16(v[8 * q + 4], v[8 * q + 5], p.c_dtype),
+                                                   pack16(v[8 * q + 6], v[8 * q + 7], p.c_dtype));
+                            }
+                        }
+                    }
+                    if (!out) continue;
+                    if (by_tma) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (p.accumulate) tma_add_3d(&p.tm_c, smem_u32(buf), col, row, tile.c2);
+                            else tma_store_3d(&p.tm_c, smem_u32(buf), col, row, tile.c2);
+                        }
+                    } else {
+                        __syncwarp();
+                        store_rows(p, buf, row, tile.rows_end, col, tile.c2, lane);
+                        __syncwarp();
+                    }
+                    if (lane == 0) bulk_commit();
+                    ++seq;
+                }
+            }
+            if (kCe && mine && row + lane < p.M)
+                p.ce.sums[static_cast<int64_t>(tile.col0 / BN) * p.M + row + lane] = make_float2(rs.top, rs.sum);
+            if (live) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (kPair) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty_bar[acc]), 0));
+                    else mbar_arrive(smem_u32(&tempty_bar[acc]));
+                }
+            }
+        }
+        // the output stores complete before the CTA exits
+        if (lane == 0) bulk_wait_all();
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    __syncwarp();
+    if (kPair) cluster_sync_all();
+    else __syncthreads();
+    tc_fence_after();
+    if (warp == 1) {
+        __syncwarp();
+        if (kPair) tmem_dealloc_pair(tmem_base, TMEM_COLS);
+        else tmem_dealloc(tmem_base, TMEM_COLS);
+    }
+}
+
+template <bool kCe>
+__global__ void __launch_bounds__(NUM_THREADS, 1) train_gemm_kernel(const __grid_constant__ GemmParams p) {
+    train_gemm_body<false, kCe>(p);
+}
+
+template <bool kCe>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
+    train_gemm_pair_kernel(const __grid_constant__ GemmParams p) {
+    train_gemm_body<true, kCe>(p);
+}
+
+// GROUP_K: a copy of A's and B's tensor map for every group, its row extent
+// cut at the group's end.  Also clears the status word.
+struct GroupMapParams {
+    CUtensorMap a, b;
+    CUtensorMap* out;
+    const void* offsets;
+    int* status;
+    int32_t groups, offsets64, rows;
+};
+
+__global__ void group_maps_kernel(const __grid_constant__ GroupMapParams p) {
+    pdl_wait_then_release();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
+    const int i = blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= 2 * p.groups) return;
+    const int64_t o = load_index(p.offsets, p.offsets64, (i >> 1) + 1);
+    const uint32_t end = o < 1 ? 1u : o > p.rows ? static_cast<uint32_t>(p.rows) : static_cast<uint32_t>(o);
+    const uint4* src = reinterpret_cast<const uint4*>(i & 1 ? &p.b : &p.a);
+    uint4* dst = reinterpret_cast<uint4*>(p.out + i);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) dst[k] = src[k];
+    asm volatile("tensormap.replace.tile.global_dim.global.b1024.b32 [%0], 1, %1;" ::"l"(dst), "r"(end) : "memory");
+    asm volatile("fence.proxy.tensormap::generic.release.gpu;" ::: "memory");
 }
 
 __global__ void pack_kernel(const uint16_t* src, int64_t src_ld, uint16_t* dst, int64_t dst_ld, int64_t rows,
@@ -99,18 +611,222 @@ __global__ void pack_kernel(const uint16_t* src, int64_t src_ld, uint16_t* dst, 
         for (int64_t c = threadIdx.x; c < cols; c += blockDim.x) dst[r * dst_ld + c] = src[r * src_ld + c];
 }
 
+// out = alpha * sum over the splits, in order.
+template <int DT>
+__global__ void split_sum_kernel(const float* parts, int64_t ld, int64_t stride, int splits, float alpha,
+                                 const float* alpha_dev, void* out, int64_t out_ld, int64_t rows, int64_t cols) {
+    pdl_wait_then_release();
+    const float f = alpha_dev ? alpha * *alpha_dev : alpha;
+    const int64_t n = rows * cols;
+    for (int64_t i = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; i < n; i += int64_t(gridDim.x) * blockDim.x) {
+        const int64_t r = i / cols, c = i - r * cols;
+        float s = 0.f;
+        for (int k = 0; k < splits; ++k) s += parts[k * stride + r * ld + c];
+        static_cast<typename Elem<DT>::T*>(out)[r * out_ld + c] = Elem<DT>::store(f * s);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+CUtensorMapDataType map_type(int dtype) {
+    return dtype == MUON_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+           : dtype == MUON_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+}
+
+// [count][rows][inner] with boxes of 128 bytes x box_rows, swizzled.
+bool map3(CUtensorMap* map, const void* base, int dtype, int64_t inner, int64_t rows, int64_t count, int64_t ld,
+          int64_t stride, uint32_t box_rows) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    const int64_t e = static_cast<int64_t>(dtype_bytes(dtype));
+    if (count <= 1) stride = rows * ld;  // unused, but must be a multiple of 16 bytes
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(count)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * e), static_cast<cuuint64_t>(stride * e)};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / e), box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, map_type(dtype), 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The same matrices as [count][inner / 64][rows][64], two 64-wide chunks of
+// 64 rows a copy: MN-major operands whose width is a multiple of 64.
+bool map_chunked(CUtensorMap* map, const void* base, int dtype, int64_t inner, int64_t rows, int64_t count, int64_t ld,
+                 int64_t stride) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    if (count <= 1) stride = rows * ld;
+    cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(inner / 64),
+                          static_cast<cuuint64_t>(count)};
+    cuuint64_t strides[3] = {static_cast<cuuint64_t>(ld * 2), 128, static_cast<cuuint64_t>(stride * 2)};
+    cuuint32_t box[4] = {64, BK, 2, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(map, map_type(dtype), 4, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Kernel attributes and the pair occupancy, set up once per device (with
+// that device current) and remembered.
+cudaError_t setup(int* max_pairs) {
+    constexpr int kMaxDevices = 64;
+    static std::mutex mu;
+    static bool done[kMaxDevices] = {};
+    static cudaError_t err[kMaxDevices] = {};
+    static int pairs[kMaxDevices] = {};
+    int dev = 0;
+    const cudaError_t dev_err = cudaGetDevice(&dev);
+    if (dev_err != cudaSuccess) return dev_err;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!done[dev]) {
+        const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+        cudaError_t e = cudaFuncSetAttribute(train_gemm_kernel<false>, attr, Ring<false>::SMEM_BYTES);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(train_gemm_kernel<true>, attr, Ring<false>::SMEM_BYTES);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(train_gemm_pair_kernel<false>, attr, Ring<true>::SMEM_BYTES);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(train_gemm_pair_kernel<true>, attr, Ring<true>::SMEM_BYTES);
+        if (e == cudaSuccess) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(2, 1, 1);
+            cfg.blockDim = dim3(NUM_THREADS, 1, 1);
+            cfg.dynamicSmemBytes = Ring<true>::SMEM_BYTES;
+            e = cudaOccupancyMaxActiveClusters(&pairs[dev], train_gemm_pair_kernel<false>, &cfg);
+        }
+        err[dev] = e;
+        done[dev] = true;
+    }
+    *max_pairs = pairs[dev];
+    return err[dev];
+}
+
+// Pairs halve each SM's operand traffic but work on 256 rows at a time.
+bool use_pairs(const TrainGemm& g) {
+    if (g.group == GROUP_M) return g.M >= g.groups * 256;
+    return g.M > BM;
+}
+
 }  // namespace
 
+int64_t train_gemm_tiles(int64_t M, int64_t N) {
+    const int64_t tm = M > BM ? 2 * BM : BM;
+    return ((M + tm - 1) / tm) * ((N + BN - 1) / BN);
+}
+
+size_t train_gemm_group_bytes(int64_t groups) { return static_cast<size_t>(groups) * 2 * sizeof(CUtensorMap); }
+
+int64_t train_gemm_col_tiles(int64_t N) { return (N + BN - 1) / BN; }
+
 cudaError_t train_gemm(const TrainGemm& g, int num_sms, cudaStream_t st) {
-    int64_t ty = (g.M + TS - 1) / TS;
-    if (g.group == GROUP_M) ty += g.groups + 2;
-    if (g.group == GROUP_K) ty *= g.groups;
-    const dim3 grid(static_cast<unsigned>((g.N + TS - 1) / TS), static_cast<unsigned>(ty));
+    int max_pairs = 0;
+    cudaError_t e = setup(&max_pairs);
+    if (e != cudaSuccess) return e;
+    const bool pair = use_pairs(g);
+    GemmParams p;
+    memset(&p, 0, sizeof p);
+    const int64_t b_count = g.group == GROUP_M ? g.groups : 1;
+    bool ok = true;
+    // the widths of MN-major operands are rounded up where the row pitch
+    // allows it: what lies past them enters only rows or columns of C that
+    // are not stored
+    const int64_t wa = g.a_mn && g.lda >= round_up(g.M, 64) && g.a_padded ? round_up(g.M, 64) : g.M;
+    const int64_t wb = g.b_mn && g.ldb >= round_up(g.N, 64) && g.b_padded ? round_up(g.N, 64) : g.N;
+    p.chunked_a = g.a_mn && wa % 64 == 0;
+    p.chunked_b = g.b_mn && wb % 64 == 0;
+    if (!g.a_mn) ok &= map3(&p.tm_a, g.A, g.dtype, g.K, g.M, 1, g.lda, 0, BM);
+    else if (p.chunked_a) ok &= map_chunked(&p.tm_a, g.A, g.dtype, wa, g.K, 1, g.lda, 0);
+    else ok &= map3(&p.tm_a, g.A, g.dtype, g.M, g.K, 1, g.lda, 0, BK);
+    if (!g.b_mn) ok &= map3(&p.tm_b, g.B, g.dtype, g.K, g.N, b_count, g.ldb, g.b_stride, pair ? BN / 2 : BN);
+    else if (p.chunked_b) ok &= map_chunked(&p.tm_b, g.B, g.dtype, wb, g.K, b_count, g.ldb, g.b_stride);
+    else ok &= map3(&p.tm_b, g.B, g.dtype, g.N, g.K, b_count, g.ldb, g.b_stride, BK);
+    const int64_t c_count = g.group == GROUP_K ? g.groups : g.splits > 1 ? g.splits : 1;
+    const int64_t ce = static_cast<int64_t>(dtype_bytes(g.c_dtype));
+    p.tma_c = g.C && (reinterpret_cast<uintptr_t>(g.C) & 15) == 0 && g.ldc * ce % 16 == 0 &&
+              (c_count <= 1 || g.c_stride * ce % 16 == 0);
+    if (p.tma_c) ok &= map3(&p.tm_c, g.C, g.c_dtype, g.N, g.M, c_count, g.ldc, g.c_stride, 32);
+    if (!ok) return cudaErrorInvalidValue;
+    const int tile_m = pair ? 2 * BM : BM;
+    p.offsets = g.offsets;
+    p.C = g.C;
+    p.alpha_dev = g.alpha_dev;
+    p.status = g.status;
+    p.ce = g.ce;
+    p.ldc = g.ldc;
+    p.c_stride = g.c_stride;
+    p.M = static_cast<int32_t>(g.M);
+    p.N = static_cast<int32_t>(g.N);
+    p.K = static_cast<int32_t>(g.K);
+    p.tiles_n = static_cast<int32_t>((g.N + BN - 1) / BN);
+    p.tiles_m = static_cast<int32_t>((g.M + tile_m - 1) / tile_m);
+    p.groups = static_cast<int32_t>(g.groups);
+    p.group = g.group;
+    p.offsets64 = g.offsets64;
+    p.c_dtype = g.c_dtype;
+    p.accumulate = g.accumulate;
+    p.a_mn = g.a_mn;
+    p.b_mn = g.b_mn;
+    p.alpha = g.alpha;
+    p.idesc = (1u << 4) | (g.dtype == MUON_BF16 ? (1u << 7) | (1u << 10) : 0u) | ((g.a_mn ? 1u : 0u) << 15) |
+              ((g.b_mn ? 1u : 0u) << 16);
+    const int64_t kb = (g.K + BK - 1) / BK;
+    int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
+    if (g.group == GROUP_M) {
+        tiles += (g.groups + 2) * static_cast<int64_t>(p.tiles_n);  // a bound: each group may end inside a tile
+    } else if (g.group == GROUP_K) {
+        tiles *= g.groups;
+    } else {
+        const int64_t splits = g.splits > 1 ? g.splits : 1;
+        p.k_blocks = static_cast<int32_t>((kb + splits - 1) / splits);
+        tiles *= splits;
+    }
+    if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+    p.total_tiles = static_cast<int32_t>(tiles);
+    // all rows of tiles together while the A operand stays in L2 (so that B
+    // is read once), else bands of 8 that share both operands' tiles
+    p.band = g.M * g.K * 2 <= (int64_t(48) << 20) ? p.tiles_m : 8;
+    if (g.group == GROUP_K) {
+        GroupMapParams m;
+        memset(&m, 0, sizeof m);
+        m.a = p.tm_a;
+        m.b = p.tm_b;
+        m.out = static_cast<CUtensorMap*>(g.group_maps);
+        m.offsets = g.offsets;
+        m.status = g.status;
+        m.groups = p.groups;
+        m.offsets64 = g.offsets64;
+        m.rows = p.K;
+        p.group_maps = m.out;
+        launch_begin(g.kind, st);
+        e = launch_pdl(group_maps_kernel, dim3((2 * p.groups + 63) / 64), dim3(64), 0, st, m);
+        launch_end(g.kind, st);
+        if (e != cudaSuccess) return e;
+    }
     launch_begin(g.kind, st);
-    if (g.dtype == MUON_BF16) gemm_kernel<MUON_BF16><<<grid, 256, 0, st>>>(g);
-    else gemm_kernel<MUON_F16><<<grid, 256, 0, st>>>(g);
+    if (pair) {
+        int64_t n = max_pairs > 0 ? max_pairs : num_sms / 2;
+        if (tiles < n) n = tiles;
+        e = launch_pdl(g.ce.sums ? train_gemm_pair_kernel<true> : train_gemm_pair_kernel<false>,
+                       dim3(static_cast<unsigned>(2 * n)), dim3(NUM_THREADS), Ring<true>::SMEM_BYTES, st, p);
+    } else {
+        const int64_t n = tiles < num_sms ? tiles : num_sms;
+        e = launch_pdl(g.ce.sums ? train_gemm_kernel<true> : train_gemm_kernel<false>, dim3(static_cast<unsigned>(n)),
+                       dim3(NUM_THREADS), Ring<false>::SMEM_BYTES, st, p);
+    }
     launch_end(g.kind, st);
-    return cudaGetLastError();
+    return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+cudaError_t launch_split_sum(const float* parts, int64_t ld, int64_t stride, int splits, float alpha,
+                             const float* alpha_dev, void* out, int64_t out_ld, int out_dtype, int64_t rows,
+                             int64_t cols, int kind, int num_sms, cudaStream_t st) {
+    const int64_t blocks = (rows * cols + 255) / 256;
+    const dim3 grid(static_cast<unsigned>(blocks < num_sms * 8 ? blocks : num_sms * 8));
+    launch_begin(kind, st);
+    const cudaError_t e =
+        launch_pdl(out_dtype == MUON_BF16 ? split_sum_kernel<MUON_BF16> : split_sum_kernel<MUON_F16>, grid, dim3(256), 0,
+                   st, parts, ld, stride, splits, alpha, alpha_dev, out, out_ld, rows, cols);
+    launch_end(kind, st);
+    return e;
 }
 
 cudaError_t launch_pack(const void* src, int64_t src_ld, void* dst, int64_t dst_ld, int64_t rows, int64_t cols,
