@@ -49,7 +49,7 @@ struct EmbedLookup {
     int32_t table_dtype, out_dtype, ids64;
     float scale;
 };
-cudaError_t launch_embed_lookup(const EmbedLookup& a, int num_sms, cudaStream_t st);
+cudaError_t launch_embed_lookup(const EmbedLookup& a, cudaStream_t st);
 
 struct EmbedGrad {
     const void* grad;
@@ -59,7 +59,7 @@ struct EmbedGrad {
     int32_t grad_dtype, ids64, accumulate;
     float scale;
 };
-size_t embed_grad_workspace(int64_t tokens, int64_t vocab, int64_t dim);
+size_t embed_grad_workspace(int64_t tokens, int64_t dim);
 cudaError_t launch_embed_grad(const EmbedGrad& a, void* workspace, int num_sms, cudaStream_t st);
 
 // ---- matrix products (train_gemm.cu) ---------------------------------------

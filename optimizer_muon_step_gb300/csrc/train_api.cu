@@ -115,14 +115,14 @@ muon_status_t muon_embedding_lookup(const void* table, int32_t table_dtype, int6
     a.out_dtype = out_dtype;
     a.ids64 = ids_dtype == MUON_I64;
     a.scale = scale;
-    return from_cuda(launch_embed_lookup(a, num_sms, st));
+    return from_cuda(launch_embed_lookup(a, st));
 }
 
 size_t muon_embedding_grad_workspace(int64_t tokens, int64_t vocab, int64_t dim) {
     if (tokens < 0 || vocab <= 0 || dim <= 0 || vocab >= (int64_t(1) << 31) || tokens >= (int64_t(1) << 31) ||
         dim > kMaxExtent)
         return 0;
-    return embed_grad_workspace(tokens, vocab, dim);
+    return embed_grad_workspace(tokens, dim);
 }
 
 muon_status_t muon_embedding_grad(const void* grad, int32_t grad_dtype, int64_t grad_ld, const void* ids,

@@ -7,7 +7,6 @@ that are not given are allocated by torch on the stream of the call.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 _P = ctypes.c_void_p
@@ -48,36 +47,52 @@ EXPORTS = ("muon_embedding_lookup", "muon_embedding_grad_workspace", "muon_embed
            "muon_expert_matmul", "muon_expert_wgrad_workspace", "muon_expert_wgrad")
 
 
-def _pkg():
-    import optimizer_muon_step_gb300 as m
-    return m
+# torch, the dtype codes and the library, bound at the first call
+torch = None
+_DT = {}
+_HALF = ()
+_lib = None
 
 
-def _dtypes():
-    import torch
-    return {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+def _bind():
+    global torch, _DT, _HALF, _lib
+    import torch as _torch
+
+    from . import load_library
+    _lib = load_library()
+    _DT = {_torch.float32: 0, _torch.bfloat16: 1, _torch.float16: 2}
+    _HALF = (_torch.bfloat16, _torch.float16)
+    torch = _torch
+
+
+def _check(status, where):
+    if status != 0:
+        from . import MuonError
+        raise MuonError(status, where)
 
 
 def _rows(t, name, dtypes, cols=None, rows=None):
     """A CUDA matrix whose rows are contiguous; its row pitch."""
-    import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
-    if t.dim() != 2 or (cols is not None and t.shape[1] != cols) or (rows is not None and t.shape[0] != rows):
-        raise ValueError(f"{name} must be a matrix of shape ({rows or 'any'}, {cols or 'any'}), got {tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    shape = t.shape
+    if len(shape) != 2 or (cols is not None and shape[1] != cols) or (rows is not None and shape[0] != rows):
+        raise ValueError(f"{name} must be a matrix of shape ({rows if rows is not None else 'any'}, "
+                         f"{cols if cols is not None else 'any'}), got {tuple(shape)}")
+    ld, step = t.stride()
+    n, c = shape
+    if c > 1 and step != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    if t.shape[0] <= 1:
-        return t.shape[1]
-    if t.stride(0) < t.shape[1]:
+    if n <= 1:
+        return c
+    if ld < c:
         raise ValueError(f"{name} must have rows that do not overlap")
-    return t.stride(0)
+    return ld
 
 
 def _index(t, name, n=None):
-    import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype not in (torch.int32, torch.int64):
@@ -89,7 +104,6 @@ def _index(t, name, n=None):
 
 def _out(t, name, shape, dtypes, device):
     """`t` checked as a contiguous output of `shape`, or a new one of dtypes[0]."""
-    import torch
     if t is None:
         return torch.empty(shape, dtype=dtypes[0], device=device)
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in dtypes:
@@ -99,22 +113,34 @@ def _out(t, name, shape, dtypes, device):
     return t
 
 
-def _on(stream):
-    """Makes `stream` (None: the current one) torch's allocation stream, so
-    that outputs and workspaces made inside belong to it."""
-    import torch
-    if stream is None:
-        return contextlib.nullcontext()
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream))
-    return torch.cuda.stream(stream)
+class _On:
+    """Makes `stream` torch's allocation stream, so that outputs and
+    workspaces made inside belong to it; its handle is the context's value.
+    None is the current stream, as it is."""
+    __slots__ = ("ctx", "raw")
+
+    def __init__(self, stream):
+        self.ctx = None
+        if stream is None:  # torch.cuda.current_stream().cuda_stream, without its 3 us
+            self.raw = torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+            return
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream))
+        self.ctx, self.raw = torch.cuda.stream(stream), stream.cuda_stream
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self.raw
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
 
 
-def _workspace(workspace, need, where, device):
-    m = _pkg()
-    if need == 0:
-        raise m.MuonError(1, where)
-    return m.allocate_workspace(need, device) if workspace is None else workspace
+def _workspace(need, where, device):
+    _check(1 if need == 0 else 0, where)
+    return torch.empty(need, dtype=torch.uint8, device=device)
 
 
 def muon_embedding_lookup(table, ids, scale: float = 1.0, padding_idx=None, out=None, out_dtype=None, stream=None):
@@ -122,22 +148,24 @@ def muon_embedding_lookup(table, ids, scale: float = 1.0, padding_idx=None, out=
 
     table: (vocab, dim) fp32, bf16 or fp16; ids: int32 or int64 of any shape.
     Ids equal to `padding_idx`, and ids outside the table, give zero rows."""
-    m = _pkg()
-    dts = _dtypes()
-    ld = _rows(table, "table", dts)
+    if _lib is None:
+        _bind()
+    ld = _rows(table, "table", _DT)
     is64 = _index(ids, "ids")
     vocab, dim = table.shape
-    with _on(stream):
+    n = ids.numel()
+    with _On(stream) as st:
         if out is None:
-            out = table.new_empty((*ids.shape, dim), dtype=out_dtype or table.dtype)
-            o, old = out, dim
+            o = out = torch.empty((*ids.shape, dim), dtype=out_dtype or table.dtype, device=table.device)
+            if o.dtype not in _DT:
+                raise TypeError(f"out_dtype {o.dtype} is not one of {tuple(_DT)}")
+            old = dim
         else:
             o = out if out.dim() == 2 else out.view(-1, dim)
-            old = _rows(o, "out", dts, dim, ids.numel())
-        m._check(m.load_library().muon_embedding_lookup(
-            table.data_ptr(), dts[table.dtype], ld, vocab, dim, ids.data_ptr(), is64, ids.numel(), scale,
-            -1 if padding_idx is None else int(padding_idx), o.data_ptr(), dts[o.dtype], old, m._stream(stream)),
-            "muon_embedding_lookup")
+            old = _rows(o, "out", _DT, dim, n)
+        _check(_lib.muon_embedding_lookup(table.data_ptr(), _DT[table.dtype], ld, vocab, dim, ids.data_ptr(), is64, n,
+                                          scale, -1 if padding_idx is None else padding_idx, o.data_ptr(),
+                                          _DT[o.dtype], old, st), "muon_embedding_lookup")
     return out
 
 
@@ -146,50 +174,46 @@ def muon_embedding_grad(grad, ids, vocab: int, scale: float = 1.0, padding_idx=N
     """The lookup's gradient as a dense fp32 (vocab, dim) table: row v is
     scale * the sum of `grad`'s rows whose id is v (added to `out` with
     `accumulate`).  grad: (*ids.shape, dim) or (tokens, dim)."""
-    import torch
-    m = _pkg()
-    dts = _dtypes()
+    if _lib is None:
+        _bind()
     is64 = _index(ids, "ids")
-    g = grad if grad.dim() == 2 else grad.reshape(-1, grad.shape[-1])
-    ld = _rows(g, "grad", dts, None, ids.numel())
+    n = ids.numel()
+    g = grad if grad.dim() == 2 else grad.view(-1, grad.shape[-1])
+    ld = _rows(g, "grad", _DT, None, n)
     dim = g.shape[1]
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
-    with _on(stream):
-        out = _out(out, "out", (int(vocab), dim), (torch.float32,), g.device)
-        lib = m.load_library()
-        ws = _workspace(workspace, lib.muon_embedding_grad_workspace(ids.numel(), int(vocab), dim),
-                        "muon_embedding_grad", g.device)
-        m._check(lib.muon_embedding_grad(g.data_ptr(), dts[g.dtype], ld, ids.data_ptr(), is64, ids.numel(), int(vocab),
-                                         dim, scale, -1 if padding_idx is None else int(padding_idx),
-                                         int(bool(accumulate)), out.data_ptr(), ws.data_ptr(), ws.numel(),
-                                         m._stream(stream)), "muon_embedding_grad")
+    with _On(stream) as st:
+        out = _out(out, "out", (vocab, dim), (torch.float32,), g.device)
+        ws = workspace
+        if ws is None:
+            ws = _workspace(_lib.muon_embedding_grad_workspace(n, vocab, dim), "muon_embedding_grad", g.device)
+        _check(_lib.muon_embedding_grad(g.data_ptr(), _DT[g.dtype], ld, ids.data_ptr(), is64, n, vocab, dim, scale,
+                                        -1 if padding_idx is None else padding_idx, 1 if accumulate else 0,
+                                        out.data_ptr(), ws.data_ptr(), ws.numel(), st), "muon_embedding_grad")
     return out
 
 
 def _ce_struct(hidden, weight, targets, logit_scale, ignore_index):
-    import torch
-    dts = _dtypes()
-    half = (torch.bfloat16, torch.float16)
-    hld = _rows(hidden, "hidden", half)
-    n, d = hidden.shape
-    wld = _rows(weight, "weight", (hidden.dtype,), d)
+    if _lib is None:
+        _bind()
     p = LinearCe()
+    p.hidden_ld = _rows(hidden, "hidden", _HALF)
+    n, d = hidden.shape
+    p.weight_ld = _rows(weight, "weight", (hidden.dtype,), d)
+    p.targets_dtype = _index(targets, "targets", n)
     p.hidden, p.weight, p.targets = hidden.data_ptr(), weight.data_ptr(), targets.data_ptr()
     p.tokens, p.vocab, p.dim = n, weight.shape[0], d
-    p.hidden_ld, p.weight_ld = hld, wld
-    p.ignore_index = int(ignore_index)
-    p.dtype = p.d_weight_dtype = dts[hidden.dtype]
-    p.targets_dtype = _index(targets, "targets", n)
-    p.logit_scale = float(logit_scale)
+    p.ignore_index = ignore_index
+    p.dtype = p.d_weight_dtype = _DT[hidden.dtype]
+    p.logit_scale = logit_scale
     return p
 
 
 def muon_linear_ce_workspace(hidden, weight, targets, with_grad: bool, budget_bytes: int = 8 << 30) -> int:
     """Workspace bytes of muon_linear_ce or (with_grad) muon_linear_ce_grad."""
     p = _ce_struct(hidden, weight, targets, 1.0, -1)
-    return int(_pkg().load_library().muon_linear_ce_workspace(ctypes.addressof(p), int(bool(with_grad)),
-                                                              int(budget_bytes)))
+    return int(_lib.muon_linear_ce_workspace(ctypes.addressof(p), 1 if with_grad else 0, int(budget_bytes)))
 
 
 def muon_linear_ce(hidden, weight, targets, logit_scale: float = 1.0, ignore_index: int = -100, loss=None, lse=None,
@@ -197,20 +221,17 @@ def muon_linear_ce(hidden, weight, targets, logit_scale: float = 1.0, ignore_ind
     """(loss, lse), fp32 per token, of the softmax over logit_scale * hidden
     weight^T.  hidden: (tokens, dim), weight: (vocab, dim), both bf16 or
     both fp16; targets: int32 or int64.  Ignored tokens have loss 0."""
-    import torch
-    m = _pkg()
     p = _ce_struct(hidden, weight, targets, logit_scale, ignore_index)
-    with _on(stream):
-        loss = _out(loss, "loss", (p.tokens,), (torch.float32,), hidden.device)
-        lse = _out(lse, "lse", (p.tokens,), (torch.float32,), hidden.device)
+    dev = hidden.device
+    with _On(stream) as st:
+        loss = _out(loss, "loss", (p.tokens,), (torch.float32,), dev)
+        lse = _out(lse, "lse", (p.tokens,), (torch.float32,), dev)
         p.loss, p.lse = loss.data_ptr(), lse.data_ptr()
-        lib = m.load_library()
         at = ctypes.addressof(p)
         ws = workspace
         if ws is None:
-            ws = _workspace(None, lib.muon_linear_ce_workspace(at, 0, int(budget_bytes)), "muon_linear_ce",
-                            hidden.device)
-        m._check(lib.muon_linear_ce(at, ws.data_ptr(), ws.numel(), m._stream(stream)), "muon_linear_ce")
+            ws = _workspace(_lib.muon_linear_ce_workspace(at, 0, budget_bytes), "muon_linear_ce", dev)
+        _check(_lib.muon_linear_ce(at, ws.data_ptr(), ws.numel(), st), "muon_linear_ce")
     return loss, lse
 
 
@@ -221,29 +242,26 @@ def muon_linear_ce_grad(hidden, weight, targets, row_scale=None, logit_scale: fl
     gradients of sum(row_scale * loss).  row_scale: fp32 per token, e.g. 1 /
     (number of counted tokens) for the mean; None means 1.  `d_weight` may be
     given as an fp32 tensor, and then be added to with `accumulate`."""
-    import torch
-    m = _pkg()
     p = _ce_struct(hidden, weight, targets, logit_scale, ignore_index)
+    dev = hidden.device
     if row_scale is not None:
-        _out(row_scale, "row_scale", (p.tokens,), (torch.float32,), hidden.device)
+        _out(row_scale, "row_scale", (p.tokens,), (torch.float32,), dev)
         p.row_scale = row_scale.data_ptr()
     if accumulate and (d_weight is None or d_weight.dtype != torch.float32):
         raise ValueError("accumulate needs an fp32 d_weight")
-    with _on(stream):
-        dev = hidden.device
+    with _On(stream) as st:
         loss = _out(loss, "loss", (p.tokens,), (torch.float32,), dev)
         lse = _out(lse, "lse", (p.tokens,), (torch.float32,), dev)
         d_hidden = _out(d_hidden, "d_hidden", hidden.shape, (hidden.dtype,), dev)
         d_weight = _out(d_weight, "d_weight", weight.shape, (hidden.dtype, torch.float32), dev)
         p.loss, p.lse, p.d_hidden, p.d_weight = (x.data_ptr() for x in (loss, lse, d_hidden, d_weight))
-        p.d_weight_dtype = _dtypes()[d_weight.dtype]
-        p.accumulate = int(bool(accumulate))
-        lib = m.load_library()
+        p.d_weight_dtype = _DT[d_weight.dtype]
+        p.accumulate = 1 if accumulate else 0
         at = ctypes.addressof(p)
         ws = workspace
         if ws is None:
-            ws = _workspace(None, lib.muon_linear_ce_workspace(at, 1, int(budget_bytes)), "muon_linear_ce_grad", dev)
-        m._check(lib.muon_linear_ce_grad(at, ws.data_ptr(), ws.numel(), m._stream(stream)), "muon_linear_ce_grad")
+            ws = _workspace(_lib.muon_linear_ce_workspace(at, 1, budget_bytes), "muon_linear_ce_grad", dev)
+        _check(_lib.muon_linear_ce_grad(at, ws.data_ptr(), ws.numel(), st), "muon_linear_ce_grad")
     return loss, lse, d_hidden, d_weight
 
 
@@ -252,32 +270,29 @@ def muon_expert_matmul(x, weight, offsets, transpose: bool = False, out=None, wo
     gradient) for the rows t in [offsets[e], offsets[e + 1]) of expert e.
     x: (tokens, cols) (or (tokens, rows)); weight: (experts, rows, cols)
     contiguous; both bf16 or both fp16.  Rows of no expert become zeros."""
-    import torch
-    m = _pkg()
-    dts = _dtypes()
-    half = (torch.bfloat16, torch.float16)
-    ld = _rows(x, "x", half)
+    if _lib is None:
+        _bind()
+    ld = _rows(x, "x", _HALF)
     if not isinstance(weight, torch.Tensor) or weight.dim() != 3:
         raise ValueError("weight must be a tensor of shape (experts, rows, cols)")
     e, r, c = weight.shape
-    _out(weight, "weight", (e, r, c), (x.dtype,), x.device)
+    _out(weight, "weight", (e, r, c), (x.dtype,), None)
+    n, width = x.shape
     xc, yc = (r, c) if transpose else (c, r)
-    if x.shape[1] != xc:
-        raise ValueError(f"x must have {xc} columns, got {x.shape[1]}")
+    if width != xc:
+        raise ValueError(f"x must have {xc} columns, got {width}")
     is64 = _index(offsets, "offsets", e + 1)
-    n = x.shape[0]
-    with _on(stream):
+    tr = 1 if transpose else 0
+    with _On(stream) as st:
         if out is None:
-            out, old = x.new_empty((n, yc)), yc
+            out, old = torch.empty((n, yc), dtype=x.dtype, device=x.device), yc
         else:
             old = _rows(out, "out", (x.dtype,), yc, n)
-        lib = m.load_library()
-        tr = int(bool(transpose))
-        ws = _workspace(workspace, lib.muon_expert_matmul_workspace(x.data_ptr(), ld, weight.data_ptr(), e, n, r, c, tr),
-                        "muon_expert_matmul", x.device)
-        m._check(lib.muon_expert_matmul(x.data_ptr(), ld, weight.data_ptr(), offsets.data_ptr(), is64, dts[x.dtype], e, n,
-                                        r, c, tr, out.data_ptr(), old, ws.data_ptr(), ws.numel(), m._stream(stream)),
-                 "muon_expert_matmul")
+        xp, wp, ws = x.data_ptr(), weight.data_ptr(), workspace
+        if ws is None:
+            ws = _workspace(_lib.muon_expert_matmul_workspace(xp, ld, wp, e, n, r, c, tr), "muon_expert_matmul", x.device)
+        _check(_lib.muon_expert_matmul(xp, ld, wp, offsets.data_ptr(), is64, _DT[x.dtype], e, n, r, c, tr,
+                                       out.data_ptr(), old, ws.data_ptr(), ws.numel(), st), "muon_expert_matmul")
     return out
 
 
@@ -287,11 +302,9 @@ def muon_expert_wgrad(grad, x, offsets, out=None, out_dtype=None, accumulate: bo
     the sum over its tokens of grad[t] x[t]^T.  grad: (tokens, rows), x:
     (tokens, cols), both bf16 or both fp16.  `out_dtype`: theirs (default)
     or fp32; `accumulate` adds to an fp32 `out`."""
-    import torch
-    m = _pkg()
-    dts = _dtypes()
-    half = (torch.bfloat16, torch.float16)
-    gld = _rows(grad, "grad", half)
+    if _lib is None:
+        _bind()
+    gld = _rows(grad, "grad", _HALF)
     n, r = grad.shape
     xld = _rows(x, "x", (grad.dtype,), None, n)
     c = x.shape[1]
@@ -299,15 +312,14 @@ def muon_expert_wgrad(grad, x, offsets, out=None, out_dtype=None, accumulate: bo
     e = offsets.numel() - 1
     if accumulate and (out is None or out.dtype != torch.float32):
         raise ValueError("accumulate needs an fp32 out")
-    with _on(stream):
+    with _On(stream) as st:
         if out is None and out_dtype is not None:
             out = torch.empty((e, r, c), dtype=out_dtype, device=x.device)
         out = _out(out, "out", (e, r, c), (grad.dtype, torch.float32), x.device)
-        lib = m.load_library()
-        ws = _workspace(workspace, lib.muon_expert_wgrad_workspace(grad.data_ptr(), gld, x.data_ptr(), xld, e, n, r, c),
-                        "muon_expert_wgrad", x.device)
-        m._check(lib.muon_expert_wgrad(grad.data_ptr(), gld, x.data_ptr(), xld, offsets.data_ptr(), is64,
-                                       dts[grad.dtype], e, n, r, c, out.data_ptr(), dts[out.dtype],
-                                       int(bool(accumulate)), ws.data_ptr(), ws.numel(), m._stream(stream)),
-                 "muon_expert_wgrad")
+        gp, xp, ws = grad.data_ptr(), x.data_ptr(), workspace
+        if ws is None:
+            ws = _workspace(_lib.muon_expert_wgrad_workspace(gp, gld, xp, xld, e, n, r, c), "muon_expert_wgrad", x.device)
+        _check(_lib.muon_expert_wgrad(gp, gld, xp, xld, offsets.data_ptr(), is64, _DT[grad.dtype], e, n, r, c,
+                                      out.data_ptr(), _DT[out.dtype], 1 if accumulate else 0, ws.data_ptr(), ws.numel(),
+                                      st), "muon_expert_wgrad")
     return out
