@@ -35,105 +35,143 @@ __device__ __forceinline__ float2 join(float2 a, float2 b) {
     return make_float2(m, sa + sb);
 }
 
-// One warp per token.
-template <int DT>
-__global__ void __launch_bounds__(256) ce_prepare_kernel(const CeBlock b) {
-    typedef typename Elem<DT>::T T;
-    pdl_wait_then_release();
-    const int lane = threadIdx.x & 31;
-    for (int64_t t = blockIdx.x * 8 + (threadIdx.x >> 5); t < b.tokens; t += gridDim.x * 8) {
-        const int64_t target = load_index(b.targets, b.targets64, t);
-        const bool inside = target >= 0 && target < b.vocab;
-        const T* h = static_cast<const T*>(b.hidden) + t * b.hidden_ld;
-        const T* w = static_cast<const T*>(b.weight) + (inside ? target : 0) * b.weight_ld;
-        T* copy = static_cast<T*>(b.packed) + t * b.packed_ld;
-        float s = 0.f;
-        for (int64_t c = lane; c < b.dim; c += 32) {
-            const T x = h[c];
-            if (b.packed) copy[c] = x;
-            s = fmaf(Elem<DT>::load(x), Elem<DT>::load(w[c]), s);
-        }
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane == 0) {
-            b.z_target[t] = inside ? b.logit_scale * s : -INFINITY;
-            if (!inside && target != b.ignore_index) *b.status = MUON_ERR_INVALID_ARG;
-        }
-    }
+// What one CTA finds out about a row: the target's logit, and the normaliser
+// in base 2 from that and the tiles' sums.
+struct Row {
+    int64_t target;
+    bool inside, live;
+    float zt, lse2;
+};
+
+// 16-byte rows on both sides?
+__device__ __forceinline__ bool wide_rows(const CeBlock& b) {
+    return ((reinterpret_cast<uintptr_t>(b.hidden) | reinterpret_cast<uintptr_t>(b.weight)) & 15) == 0 && b.dim % 8 == 0 &&
+           b.hidden_ld % 8 == 0 && b.weight_ld % 8 == 0;
 }
 
-// 32 tokens per CTA, one per lane; the warps share the column tiles.
-__global__ void __launch_bounds__(1024) ce_finish_kernel(const CeBlock b) {
-    __shared__ float2 part[32][32];
-    pdl_wait_then_release();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t t = blockIdx.x * int64_t(32) + lane;
+template <int DT, int kThreads>
+__device__ __forceinline__ Row find_row(const CeBlock& b, int64_t t) {
+    typedef typename Elem<DT>::T T;
+    __shared__ float2 part[kThreads / 32];
+    __shared__ float dot[kThreads / 32];
+    Row r;
+    r.target = load_index(b.targets, b.targets64, t);
+    r.inside = r.target >= 0 && r.target < b.vocab;
+    r.live = r.inside && r.target != b.ignore_index;
     float2 acc = make_float2(-INFINITY, 0.f);
-    if (t < b.tokens)
-        for (int64_t i = warp; i < b.col_tiles; i += 32) acc = join(acc, b.sums[i * b.tokens + t]);
-    part[warp][lane] = acc;
+    for (int64_t i = threadIdx.x; i < b.col_tiles; i += kThreads) acc = join(acc, b.sums[t * b.col_tiles + i]);
+    float s = 0.f;
+    if (r.inside) {
+        const T* h = static_cast<const T*>(b.hidden) + t * b.hidden_ld;
+        const T* w = static_cast<const T*>(b.weight) + r.target * b.weight_ld;
+        if (wide_rows(b)) {
+            for (int64_t c = 8 * threadIdx.x; c < b.dim; c += 8 * kThreads) {
+                const uint4 x = *reinterpret_cast<const uint4*>(h + c), y = *reinterpret_cast<const uint4*>(w + c);
+                const T* xe = reinterpret_cast<const T*>(&x);
+                const T* ye = reinterpret_cast<const T*>(&y);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s = fmaf(Elem<DT>::load(xe[i]), Elem<DT>::load(ye[i]), s);
+            }
+        } else {
+            for (int64_t c = threadIdx.x; c < b.dim; c += kThreads) s = fmaf(Elem<DT>::load(h[c]), Elem<DT>::load(w[c]), s);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        acc = join(acc, make_float2(__shfl_xor_sync(0xffffffffu, acc.x, o), __shfl_xor_sync(0xffffffffu, acc.y, o)));
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+    }
+    if ((threadIdx.x & 31) == 0) {
+        part[threadIdx.x >> 5] = acc;
+        dot[threadIdx.x >> 5] = s;
+    }
     __syncthreads();
-    if (warp != 0 || t >= b.tokens) return;
-    for (int i = 1; i < 32; ++i) acc = join(acc, part[i][lane]);
-    const int64_t target = load_index(b.targets, b.targets64, t);
-    const bool inside = target >= 0 && target < b.vocab;
-    const float zt = b.z_target[t];
-    if (inside) acc = join(acc, make_float2(zt * kLog2e, isnan(zt) ? zt : 1.f));
-    const float lse2 = (isinf(acc.x) ? 0.f : acc.x) + log2f(acc.y);
-    const float lse = lse2 * kLn2;
-    b.lse2[t] = lse2;
+    acc = part[0];
+    s = dot[0];
+    for (int i = 1; i < kThreads / 32; ++i) {
+        acc = join(acc, part[i]);
+        s += dot[i];
+    }
+    r.zt = b.logit_scale * s;
+    if (r.inside) acc = join(acc, make_float2(r.zt * kLog2e, isnan(r.zt) ? r.zt : 1.f));
+    r.lse2 = (isinf(acc.x) ? 0.f : acc.x) + log2f(acc.y);
+    return r;
+}
+
+__device__ __forceinline__ void put_loss(const CeBlock& b, int64_t t, const Row& r) {
+    const float lse = r.lse2 * kLn2;
     b.lse[t] = lse;
-    b.loss[t] = inside && target != b.ignore_index ? lse - zt : 0.f;
+    b.loss[t] = r.live ? lse - r.zt : 0.f;
+    if (!r.inside && r.target != b.ignore_index) atomicCAS(b.status, 0, static_cast<int>(MUON_ERR_INVALID_ARG));
+}
+
+// Loss and normaliser alone; one CTA per token.
+constexpr int kFinishThreads = 128;
+template <int DT>
+__global__ void __launch_bounds__(kFinishThreads) ce_finish_kernel(const __grid_constant__ CeBlock b) {
+    pdl_wait_then_release();
+    const Row r = find_row<DT, kFinishThreads>(b, blockIdx.x);
+    if (threadIdx.x == 0) put_loss(b, blockIdx.x, r);
 }
 
 constexpr int kRowThreads = 512;
+constexpr int kRowStep = 8 * kRowThreads;  // logits of one sweep
 
-// One CTA per token.
+// Loss, normaliser and the logits' gradient in place, and the hidden row's
+// copy for d_weight's product (zeros when ignored); one CTA per token.  Reads
+// 4 and writes 2 bytes a logit.  Sweep c reads bytes [c, c + 1) * 16 KB of the
+// row and writes [c, c + 1) * 8 KB, which sweep c / 2 has read: with a barrier
+// after the reads of sweeps 0, 1, 2, 4, 8, ... every write comes after all
+// reads of what it covers.
 template <int DT>
-__global__ void __launch_bounds__(kRowThreads) ce_grad_rows_kernel(const CeBlock b) {
+__global__ void __launch_bounds__(kRowThreads, 3) ce_grad_rows_kernel(const __grid_constant__ CeBlock b) {
     typedef typename Elem<DT>::T TG;
     pdl_wait_then_release();
     const int64_t t = blockIdx.x;
-    float* z = b.Z + t * b.z_ld;
-    TG* g = reinterpret_cast<TG*>(z);
-    const int64_t target = load_index(b.targets, b.targets64, t);
-    const bool live = target >= 0 && target < b.vocab && target != b.ignore_index;
-    const float top = *b.scale_max;
-    const float scale = ce_grad_lift(DT) * (b.row_scale ? (top > 0.f ? b.row_scale[t] / top : 0.f) : 1.f);
-    const float c2 = b.logit_scale * kLog2e, lse2 = b.lse2[t];
-    const float pt = exp2_fast(b.z_target[t] * kLog2e - lse2);
-    for (int64_t v0 = 0; v0 < b.vocab; v0 += kRowThreads) {
-        const int64_t v = v0 + threadIdx.x;
-        const float x = v < b.vocab ? z[v] : 0.f;
-        __syncthreads();  // the row's reads stay ahead of its writes, which take half the space
-        float d = v == target ? pt - 1.f : exp2_fast(fmaf(x, c2, -lse2));
-        d = live ? scale * d : 0.f;
-        if (v < b.vocab) g[v] = Elem<DT>::store(d);
-    }
-    if (!live)
-        for (int64_t c = threadIdx.x; c < b.dim; c += kRowThreads)
-            static_cast<TG*>(b.packed)[t * b.packed_ld + c] = Elem<DT>::store(0.f);
-}
-
-__global__ void ce_scale_kernel(const float* row_scale, int64_t tokens, float mult, float* out, int* status) {
-    __shared__ float red[32];
-    pdl_wait_then_release();
-    float m = row_scale ? 0.f : 1.f;
-    if (row_scale)
-        for (int64_t t = threadIdx.x; t < tokens; t += blockDim.x) {
-            const float a = fabsf(row_scale[t]);
-            m = isnan(a) || a > m ? a : m;
+    const float* z = b.Z + t * b.z_ld;
+    TG* g = reinterpret_cast<TG*>(b.Z + t * b.z_ld);
+    auto load = [&](int64_t v, float4& x, float4& y) {
+        x = y = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (v < b.vocab) {  // rows are padded to 64 logits
+            x = __ldcs(reinterpret_cast<const float4*>(z + v));
+            y = __ldcs(reinterpret_cast<const float4*>(z + v) + 1);
         }
-    for (int o = 16; o > 0; o >>= 1) {
-        const float x = __shfl_xor_sync(0xffffffffu, m, o);
-        m = isnan(x) || x > m ? x : m;
+    };
+    float4 x, y;
+    load(8 * threadIdx.x, x, y);
+    const Row r = find_row<DT, kRowThreads>(b, t);
+    if (threadIdx.x == 0) put_loss(b, t, r);
+    const TG* h = static_cast<const TG*>(b.hidden) + t * b.hidden_ld;
+    TG* copy = static_cast<TG*>(b.packed) + t * b.packed_ld;
+    if (wide_rows(b)) {
+        for (int64_t c = 8 * threadIdx.x; c < b.dim; c += 8 * kRowThreads)
+            *reinterpret_cast<uint4*>(copy + c) =
+                r.live ? *reinterpret_cast<const uint4*>(h + c) : make_uint4(0u, 0u, 0u, 0u);
+    } else {
+        for (int64_t c = threadIdx.x; c < b.dim; c += kRowThreads) copy[c] = r.live ? h[c] : Elem<DT>::store(0.f);
     }
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int i = 1; i < static_cast<int>(blockDim.x >> 5); ++i) m = isnan(red[i]) || red[i] > m ? red[i] : m;
-        out[0] = m;
-        out[1] = m * mult;
-        *status = 0;
+    const float top = b.scalars[0];
+    const float scale = ce_grad_lift(DT) * (b.row_scale ? (top > 0.f ? b.row_scale[t] / top : 0.f) : 1.f);
+    const float c2 = b.logit_scale * kLog2e;
+    const float hot = exp2_fast(r.zt * kLog2e - r.lse2) - 1.f;
+    int sweep = 0;
+    for (int64_t v0 = 0; v0 < b.vocab; v0 += kRowStep, ++sweep) {
+        const int64_t v = v0 + 8 * threadIdx.x;
+        float4 nx, ny;
+        load(v + kRowStep, nx, ny);
+        if ((sweep & (sweep - 1)) == 0) __syncthreads();
+        if (v < b.vocab) {
+            float d[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+            TG out[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float p = v + i == r.target ? hot : exp2_fast(fmaf(d[i], c2, -r.lse2));
+                out[i] = Elem<DT>::store(r.live && v + i < b.vocab ? scale * p : 0.f);
+            }
+            *reinterpret_cast<uint4*>(g + v) = *reinterpret_cast<const uint4*>(out);
+        }
+        x = nx;
+        y = ny;
     }
 }
 
@@ -146,20 +184,10 @@ __global__ void round_kernel(const float* src, typename Elem<DT>::T* dst, int64_
 
 }  // namespace
 
-cudaError_t launch_ce_prepare(const CeBlock& b, int num_sms, cudaStream_t st) {
-    const int64_t blocks = (b.tokens + 7) / 8;
-    const dim3 grid(static_cast<unsigned>(blocks < num_sms * 8 ? blocks : num_sms * 8));
-    launch_begin(MUON_KERNEL_CE_ROWS, st);
-    const cudaError_t e = launch_pdl(b.dtype == MUON_BF16 ? ce_prepare_kernel<MUON_BF16> : ce_prepare_kernel<MUON_F16>,
-                                     grid, dim3(256), 0, st, b);
-    launch_end(MUON_KERNEL_CE_ROWS, st);
-    return e;
-}
-
 cudaError_t launch_ce_finish(const CeBlock& b, cudaStream_t st) {
     launch_begin(MUON_KERNEL_CE_ROWS, st);
-    const cudaError_t e =
-        launch_pdl(ce_finish_kernel, dim3(static_cast<unsigned>((b.tokens + 31) / 32)), dim3(1024), 0, st, b);
+    const cudaError_t e = launch_pdl(b.dtype == MUON_BF16 ? ce_finish_kernel<MUON_BF16> : ce_finish_kernel<MUON_F16>,
+                                     dim3(static_cast<unsigned>(b.tokens)), dim3(kFinishThreads), 0, st, b);
     launch_end(MUON_KERNEL_CE_ROWS, st);
     return e;
 }
@@ -169,14 +197,6 @@ cudaError_t launch_ce_grad_rows(const CeBlock& b, cudaStream_t st) {
     const cudaError_t e =
         launch_pdl(b.dtype == MUON_BF16 ? ce_grad_rows_kernel<MUON_BF16> : ce_grad_rows_kernel<MUON_F16>,
                    dim3(static_cast<unsigned>(b.tokens)), dim3(kRowThreads), 0, st, b);
-    launch_end(MUON_KERNEL_CE_ROWS, st);
-    return e;
-}
-
-cudaError_t launch_ce_scale(const float* row_scale, int64_t tokens, float mult, float* out, int* status,
-                            cudaStream_t st) {
-    launch_begin(MUON_KERNEL_CE_ROWS, st);
-    const cudaError_t e = launch_pdl(ce_scale_kernel, dim3(1), dim3(1024), 0, st, row_scale, tokens, mult, out, status);
     launch_end(MUON_KERNEL_CE_ROWS, st);
     return e;
 }

@@ -70,15 +70,20 @@ cudaError_t launch_embed_grad(const EmbedGrad& a, void* workspace, int num_sms, 
 // with groups the ranges [offsets[e], offsets[e + 1]) of the token axis.
 enum { GROUP_NONE = 0, GROUP_M = 1, GROUP_K = 2 };
 
-// Softmax sums of the product's rows, one pair per row and 256-column tile:
+// Softmax sums of the product's rows, one pair per row and column tile:
 // (top, sum over the tile of exp2(x - top)), x = scale2 * product, without
 // the row's target column.  The product itself is stored when `store` is set.
 struct CeEpilogue {
-    float2* sums;         // [column tile][M]; null: no softmax
+    float2* sums;         // [M][column tile]; null: no softmax
     const void* targets;
     int32_t targets64;
     int32_t store;
-    float scale2;         // log2(e) * logit_scale
+    int32_t first;           // 1: the call's first product, which clears the status word and writes the scalars
+    float scale2;            // log2(e) * logit_scale
+    const float* row_scale;  // the call's, may be null
+    int64_t tokens;          // of the call
+    float* scalars;          // [0] the largest |row_scale| (1 when null), [1] that times factor
+    float factor;
 };
 
 struct TrainGemm {
@@ -107,7 +112,8 @@ struct TrainGemm {
 };
 cudaError_t train_gemm(const TrainGemm& g, int num_sms, cudaStream_t st);
 size_t train_gemm_group_bytes(int64_t groups);
-int64_t train_gemm_col_tiles(int64_t N);           // 256-column tiles
+int64_t train_gemm_col_tiles(int64_t M, int64_t N);  // column tiles of a plain product with K-major B
+int64_t train_gemm_max_col_tiles(int64_t N);         // whatever M is
 int64_t train_gemm_tiles(int64_t M, int64_t N);    // tiles of a plain product, one per CTA or CTA pair
 // out = alpha * the sum of `splits` fp32 matrices, in order.
 cudaError_t launch_split_sum(const float* parts, int64_t ld, int64_t stride, int splits, float alpha,
@@ -125,30 +131,22 @@ struct CeBlock {
     const void* weight;      // the caller's rows
     const void* targets;
     const float* row_scale;  // may be null
-    const float* scale_max;  // device: largest |row_scale|
-    const float2* sums;      // [column tile][tokens], see CeEpilogue
-    float* z_target;         // logit_scale * the target's logit
-    float* lse2;             // the normaliser in base 2
+    const float* scalars;    // see CeEpilogue
+    const float2* sums;      // [tokens][column tile], see CeEpilogue
     float* loss;
     float* lse;
     float* Z;                // logits; turned in place into the gradient's 16-bit rows
-    void* packed;            // copy of the hidden rows (null: none); ignored rows are cleared by ce_grad_rows
+    void* packed;            // copy of the hidden rows for d_weight, zeros for ignored tokens
     int* status;
     int64_t hidden_ld, weight_ld, packed_ld, z_ld;
     int64_t tokens, vocab, dim, ignore_index, col_tiles;
     int32_t targets64, dtype;
     float logit_scale;
 };
-// The targets' logits in fp32, and the packed copy.
-cudaError_t launch_ce_prepare(const CeBlock& b, int num_sms, cudaStream_t st);
-// Loss and normaliser from the tiles' sums.
+// Loss and normaliser from the tiles' sums and the target's logit.
 cudaError_t launch_ce_finish(const CeBlock& b, cudaStream_t st);
-// Logits -> their gradient.
+// The same, the logits turned into their gradient, and the packed copy.
 cudaError_t launch_ce_grad_rows(const CeBlock& b, cudaStream_t st);
-// out[0] = largest |row_scale| (1 when null), out[1] = out[0] * mult; clears
-// the status word.
-cudaError_t launch_ce_scale(const float* row_scale, int64_t tokens, float mult, float* out, int* status,
-                            cudaStream_t st);
 // The fixed factor that keeps small fp16 logit gradients out of the
 // subnormal range: |g| <= 1 is stored times 2^15 (at most 32768 < 65504).
 // bf16 has fp32's exponents and takes 1.

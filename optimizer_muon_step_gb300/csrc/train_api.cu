@@ -174,16 +174,15 @@ namespace {
 
 // Workspace: header and scalars, the packed weight (when its rows are not
 // 16-byte), the fp32 sums of d_weight (several blocks and a 16-bit result),
-// then for a block of tokens: the column tiles' softmax sums, the target
-// logits and normalisers, the packed hidden rows, and with gradients the rows
+// then for a block of tokens: the column tiles' softmax sums, the packed
+// hidden rows, and with gradients the rows
 // of logits and the pieces of d_hidden.
 struct CeLayout {
     int64_t block = 0;   // tokens per block
     int64_t z_ld = 0, h_ld = 0, w_ld = 0, part_ld = 0;
-    int64_t col_tiles = 0;
     int splits = 1;      // pieces of the vocabulary in d_hidden's product
     bool pack_w = false, pack_h = false, sums = false;
-    size_t w_off = 0, sum_off = 0, tile_off = 0, zt_off = 0, lse_off = 0, h_off = 0, z_off = 0, part_off = 0, total = 0;
+    size_t w_off = 0, sum_off = 0, tile_off = 0, h_off = 0, z_off = 0, part_off = 0, total = 0;
 };
 
 constexpr size_t kScalarsOff = 256;
@@ -224,19 +223,16 @@ size_t ce_total(const muon_linear_ce_t* p, bool grad, int64_t block, CeLayout* L
     L->z_ld = pitch64(v);
     L->h_ld = pitch64(d);
     L->part_ld = round_up(d, 4);
-    L->col_tiles = train_gemm_col_tiles(v);
     L->pack_w = !tma_ready(p->weight, p->weight_ld);
-    L->pack_h = grad || !tma_ready(p->hidden, p->hidden_ld);
+    L->pack_h = !tma_ready(p->hidden, p->hidden_ld);
     L->w_ld = L->pack_w ? pitch64(d) : p->weight_ld;
     L->sums = grad && block < p->tokens && p->d_weight_dtype != MUON_F32;
     L->splits = grad ? hidden_splits(block, d, v) : 1;
     size_t at = kFixedBytes;
     L->w_off = take(at, L->pack_w ? 2 * v * L->w_ld : 0);
     L->sum_off = take(at, L->sums ? 4 * v * d : 0);
-    L->tile_off = take(at, 8 * block * L->col_tiles);
-    L->zt_off = take(at, 4 * block);
-    L->lse_off = take(at, 4 * block);
-    L->h_off = take(at, L->pack_h ? 2 * block * L->h_ld : 0);
+    L->tile_off = take(at, 8 * block * train_gemm_max_col_tiles(v));
+    L->h_off = take(at, grad || L->pack_h ? 2 * block * L->h_ld : 0);
     L->z_off = take(at, grad ? 4 * block * L->z_ld : 0);
     L->part_off = take(at, L->splits > 1 ? 4 * L->splits * block * L->part_ld : 0);
     L->total = at;
@@ -313,10 +309,9 @@ muon_status_t ce_run(const muon_linear_ce_t* p, bool grad, void* workspace, size
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     int* status = reinterpret_cast<int*>(ws);
     float* scalars = reinterpret_cast<float*>(ws + kScalarsOff);
-    cudaError_t e = launch_ce_scale(grad ? p->row_scale : nullptr, n, p->logit_scale / ce_grad_lift(p->dtype), scalars,
-                                    status, st);
+    cudaError_t e = cudaSuccess;
     const void* weight = p->weight;
-    if (e == cudaSuccess && L.pack_w) {
+    if (L.pack_w) {
         e = launch_pack(p->weight, p->weight_ld, ws + L.w_off, L.w_ld, v, d, num_sms, st);
         weight = ws + L.w_off;
     }
@@ -329,26 +324,24 @@ muon_status_t ce_run(const muon_linear_ce_t* p, bool grad, void* workspace, size
         c.weight_ld = p->weight_ld;
         c.targets = static_cast<const uint8_t*>(p->targets) + t0 * ie;
         c.row_scale = grad && p->row_scale ? p->row_scale + t0 : nullptr;
-        c.scale_max = scalars;
+        c.scalars = scalars;
         c.sums = reinterpret_cast<const float2*>(ws + L.tile_off);
-        c.z_target = reinterpret_cast<float*>(ws + L.zt_off);
-        c.lse2 = reinterpret_cast<float*>(ws + L.lse_off);
         c.loss = p->loss + t0;
         c.lse = p->lse + t0;
         c.Z = reinterpret_cast<float*>(ws + L.z_off);
         c.z_ld = L.z_ld;
-        c.packed = L.pack_h ? ws + L.h_off : nullptr;
+        c.packed = ws + L.h_off;
         c.packed_ld = L.h_ld;
         c.status = status;
         c.tokens = m;
         c.vocab = v;
         c.dim = d;
         c.ignore_index = p->ignore_index;
-        c.col_tiles = L.col_tiles;
+        c.col_tiles = train_gemm_col_tiles(m, v);
         c.targets64 = p->targets_dtype == MUON_I64;
         c.dtype = p->dtype;
         c.logit_scale = p->logit_scale;
-        e = launch_ce_prepare(c, num_sms, st);
+        if (L.pack_h) e = launch_pack(c.hidden, p->hidden_ld, c.packed, L.h_ld, m, d, num_sms, st);
         if (e != cudaSuccess) break;
         TrainGemm g = {};
         g.A = L.pack_h ? c.packed : c.hidden;
@@ -368,13 +361,16 @@ muon_status_t ce_run(const muon_linear_ce_t* p, bool grad, void* workspace, size
         g.ce.targets = c.targets;
         g.ce.targets64 = c.targets64;
         g.ce.store = grad;
+        g.ce.first = t0 == 0;
         g.ce.scale2 = p->logit_scale * 1.4426950408889634f;
+        g.ce.row_scale = grad ? p->row_scale : nullptr;
+        g.ce.tokens = n;
+        g.ce.scalars = scalars;
+        g.ce.factor = p->logit_scale / ce_grad_lift(p->dtype);
         g.kind = MUON_KERNEL_CE_LOGITS;
         e = train_gemm(g, num_sms, st);
-        if (e == cudaSuccess) e = launch_ce_finish(c, st);
+        if (e == cudaSuccess) e = grad ? launch_ce_grad_rows(c, st) : launch_ce_finish(c, st);
         if (e != cudaSuccess || !grad) continue;
-        e = launch_ce_grad_rows(c, st);
-        if (e != cudaSuccess) break;
         // d_hidden = G W; the rows of G lie in the front halves of Z's rows
         const int splits = m == L.block ? L.splits
                                         : std::min<int>(hidden_splits(m, d, v), static_cast<int>(L.splits * L.block / m));

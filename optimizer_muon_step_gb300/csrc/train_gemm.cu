@@ -69,6 +69,8 @@ struct GemmParams {
     int64_t ldc, c_stride;          // elements
     int32_t M, N, K;                // GROUP_M: M rows in all; GROUP_K: K rows in all
     int32_t tiles_m, tiles_n, total_tiles;  // GROUP_M: tiles_m and total_tiles are found on the device
+    int32_t bn;                     // columns of a tile, a multiple of 32 (64 for 16-bit C) up to BN
+    int32_t sub_bytes;              // of one staged k-block, this CTA's part
     int32_t band;                   // rows of tiles walked together (GROUP_NONE, GROUP_K)
     int32_t groups, group, offsets64;
     int32_t k_blocks;               // per split (GROUP_NONE)
@@ -81,7 +83,7 @@ struct GemmParams {
 
 struct Tile {
     int row0, rows_end;  // first row of the (pair) tile, end of its rows
-    int col0;
+    int col0, tn;        // first column, column tile
     int c2;              // third coordinate of C: group or split
     int group;           // weight matrix (GROUP_M), tensor maps (GROUP_K)
     int k0;              // first k (elements)
@@ -118,7 +120,8 @@ struct Walker {
             const int n = rr / h;
             o.row0 = (b * p.band + rr - n * h) * TILE_M;
             o.rows_end = p.M;
-            o.col0 = n * BN;
+            o.tn = n;
+            o.col0 = n * p.bn;
             o.c2 = o.group = s;
             if (p.group == GROUP_K) {
                 const int a = clamped(p, s, p.K), e = clamped(p, s + 1, p.K);
@@ -160,7 +163,8 @@ struct Walker {
         const int g = base + src - 1;
         o.row0 = a + (r - n * tm) * TILE_M;
         o.rows_end = e;
-        o.col0 = n * BN;
+        o.tn = n;
+        o.col0 = n * p.bn;
         o.c2 = 0;
         o.group = g;
         o.k0 = 0;
@@ -169,13 +173,13 @@ struct Walker {
     }
 };
 
-// Columns the MMA computes: 256, or at the edge the next multiple of 32 (16
+// Columns the MMA computes: the tile's, or at the edge the next multiple of 32 (16
 // for single CTAs; of 128 with chunked pairs, whose halves start on a chunk).
 template <bool kPair>
 __device__ __forceinline__ int tile_cols(const GemmParams& p, int col0) {
     const int rem = p.N - col0;
     const int q = !kPair ? 15 : p.b_mn && p.chunked_b ? 127 : 31;
-    return rem < BN ? (rem + q) & ~q : BN;
+    return rem < p.bn ? (rem + q) & ~q : p.bn;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -243,6 +247,28 @@ struct RowSums {
     }
 };
 
+// The scalars of a loss call, by one warp while the first tile's products
+// are under way.
+__device__ __forceinline__ void write_scalars(const CeEpilogue& ce, int lane) {
+    float m = ce.row_scale ? 0.f : 1.f;
+    if (ce.row_scale) {
+#pragma unroll 8
+        for (int64_t t = lane; t < ce.tokens; t += 32) {
+            const float a = fabsf(ce.row_scale[t]);
+            m = isnan(a) || a > m ? a : m;
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float x = __shfl_xor_sync(0xffffffffu, m, o);
+        m = isnan(x) || x > m ? x : m;
+    }
+    if (lane == 0) {
+        ce.scalars[0] = m;
+        ce.scalars[1] = m * ce.factor;
+    }
+}
+
 template <bool kPair, bool kCe>
 __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
     typedef Ring<kPair> R;
@@ -298,9 +324,10 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
     const uint32_t tmem_base = *tmem_slot;
     // the prologue above touched only shared memory, TMEM and parameters
     pdl_wait_then_release();
-    // a GROUP_M product is a call's only kernel but for copies: it clears the
-    // status word, which a wait that runs out sets seconds later
-    if (p.group == GROUP_M && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
+    // a GROUP_M product and the logits' first one begin their call (but for
+    // copies): they clear the status word, which a wait that runs out sets
+    // seconds later
+    if ((p.group == GROUP_M || (kCe && p.ce.first)) && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
 
     Walker<R::TILE_M> walk(p, lane);
     Tile tile;
@@ -336,7 +363,7 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
                     const uint32_t fb = smem_u32(&full_bar[stage]);
                     const uint32_t fl = kPair ? mapa_shared(fb, 0) : fb;
                     const int nsub = tile.nk - kb0 < R::KPS ? tile.nk - kb0 : R::KPS;
-                    if (rank == 0) mbar_expect_tx(fb, (kPair ? 2 : 1) * R::SUB_BYTES * nsub);
+                    if (rank == 0) mbar_expect_tx(fb, (kPair ? 2 : 1) * p.sub_bytes * nsub);
                     auto load3 = [&](uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2) {
                         if (kPair) tma_load_3d_pair(dst, map, c0, c1, c2, fl);
                         else tma_load_3d(dst, map, c0, c1, c2, fl);
@@ -443,6 +470,7 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
         int local = 0;
         const float alpha = p.alpha_dev ? p.alpha * *p.alpha_dev : p.alpha;
         const int cols = p.c_dtype == MUON_F32 ? 32 : 64;
+        if (kCe && p.ce.first && blockIdx.x == 0 && ew == 0) write_scalars(p.ce, lane);
         for (int t = worker; walk.next(t, tile); t += workers) {
             const int acc = local & 1;
             const uint32_t acc_phase = static_cast<uint32_t>(local >> 1) & 1u;
@@ -464,7 +492,7 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
                 target = tg >= 0 && tg < p.N ? static_cast<int>(tg) : -1;
             }
             if (mine) {
-                for (int c = 0; c < BN; c += cols) {
+                for (int c = 0; c < p.bn; c += cols) {
                     const int col = tile.col0 + c;
                     if (col >= p.N) break;
                     const uint32_t b = seq % NSLOT;
@@ -542,7 +570,7 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
                 }
             }
             if (kCe && mine && row + lane < p.M)
-                p.ce.sums[static_cast<int64_t>(tile.col0 / BN) * p.M + row + lane] = make_float2(rs.top, rs.sum);
+                p.ce.sums[static_cast<int64_t>(row + lane) * p.tiles_n + tile.tn] = make_float2(rs.top, rs.sum);
             if (live) {
                 tc_fence_before();
                 __syncwarp();
@@ -611,18 +639,29 @@ __global__ void pack_kernel(const uint16_t* src, int64_t src_ld, uint16_t* dst, 
         for (int64_t c = threadIdx.x; c < cols; c += blockDim.x) dst[r * dst_ld + c] = src[r * src_ld + c];
 }
 
-// out = alpha * sum over the splits, in order.
+// out = alpha * sum over the splits, in order; four columns a thread (rows
+// are padded to four).
 template <int DT>
-__global__ void split_sum_kernel(const float* parts, int64_t ld, int64_t stride, int splits, float alpha,
-                                 const float* alpha_dev, void* out, int64_t out_ld, int64_t rows, int64_t cols) {
+__global__ void __launch_bounds__(256) split_sum_kernel(const float* parts, int64_t ld, int64_t stride, int splits,
+                                                        float alpha, const float* alpha_dev, void* out, int64_t out_ld,
+                                                        int64_t rows, int64_t cols) {
     pdl_wait_then_release();
     const float f = alpha_dev ? alpha * *alpha_dev : alpha;
-    const int64_t n = rows * cols;
-    for (int64_t i = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; i < n; i += int64_t(gridDim.x) * blockDim.x) {
-        const int64_t r = i / cols, c = i - r * cols;
-        float s = 0.f;
-        for (int k = 0; k < splits; ++k) s += parts[k * stride + r * ld + c];
-        static_cast<typename Elem<DT>::T*>(out)[r * out_ld + c] = Elem<DT>::store(f * s);
+    const int64_t quads = ld / 4, n = rows * quads;
+    for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) {
+        const int64_t r = i / quads, c = 4 * (i - r * quads);
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float* p = parts + r * ld + c;
+#pragma unroll 8
+        for (int k = 0; k < splits; ++k) {
+            const float4 x = *reinterpret_cast<const float4*>(p + k * stride);
+            s = make_float4(s.x + x.x, s.y + x.y, s.z + x.z, s.w + x.w);
+        }
+        typename Elem<DT>::T* o = static_cast<typename Elem<DT>::T*>(out) + r * out_ld + c;
+        const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (c + k < cols) o[k] = Elem<DT>::store(f * v[k]);
     }
 }
 
@@ -715,7 +754,29 @@ int64_t train_gemm_tiles(int64_t M, int64_t N) {
 
 size_t train_gemm_group_bytes(int64_t groups) { return static_cast<size_t>(groups) * 2 * sizeof(CUtensorMap); }
 
-int64_t train_gemm_col_tiles(int64_t N) { return (N + BN - 1) / BN; }
+// Columns of a plain product's tiles when B is K-major: the width whose tiles
+// fill the last wave of CTAs best.  16 rows against 163840 columns: 224
+// columns leave 732 tiles for 152 CTAs (4.8 waves) where 256 leave 640 (4.2).
+int64_t train_gemm_bn(int64_t M, int64_t N) {
+    const int64_t workers = M > BM ? 76 : 152, tm = M > BM ? 2 * BM : BM, rows = (M + tm - 1) / tm;
+    int64_t best = BN, cost = 0;
+    for (int64_t bn = BN; bn >= 128; bn -= 32) {
+        const int64_t waves = (rows * ((N + bn - 1) / bn) + workers - 1) / workers;
+        const int64_t c = waves * (bn + 16);
+        if (bn == BN || c < cost) {
+            best = bn;
+            cost = c;
+        }
+    }
+    return best;
+}
+
+int64_t train_gemm_col_tiles(int64_t M, int64_t N) {
+    const int64_t bn = train_gemm_bn(M, N);
+    return (N + bn - 1) / bn;
+}
+
+int64_t train_gemm_max_col_tiles(int64_t N) { return (N + 127) / 128; }
 
 cudaError_t train_gemm(const TrainGemm& g, int num_sms, cudaStream_t st) {
     int max_pairs = 0;
@@ -725,6 +786,8 @@ cudaError_t train_gemm(const TrainGemm& g, int num_sms, cudaStream_t st) {
     GemmParams p;
     memset(&p, 0, sizeof p);
     const int64_t b_count = g.group == GROUP_M ? g.groups : 1;
+    const int64_t bn = g.ce.sums ? train_gemm_bn(g.M, g.N) : BN;
+    p.bn = static_cast<int32_t>(bn);
     bool ok = true;
     // the widths of MN-major operands are rounded up where the row pitch
     // allows it: what lies past them enters only rows or columns of C that
@@ -736,7 +799,8 @@ cudaError_t train_gemm(const TrainGemm& g, int num_sms, cudaStream_t st) {
     if (!g.a_mn) ok &= map3(&p.tm_a, g.A, g.dtype, g.K, g.M, 1, g.lda, 0, BM);
     else if (p.chunked_a) ok &= map_chunked(&p.tm_a, g.A, g.dtype, wa, g.K, 1, g.lda, 0);
     else ok &= map3(&p.tm_a, g.A, g.dtype, g.M, g.K, 1, g.lda, 0, BK);
-    if (!g.b_mn) ok &= map3(&p.tm_b, g.B, g.dtype, g.K, g.N, b_count, g.ldb, g.b_stride, pair ? BN / 2 : BN);
+    if (!g.b_mn) ok &= map3(&p.tm_b, g.B, g.dtype, g.K, g.N, b_count, g.ldb, g.b_stride,
+                            static_cast<uint32_t>(pair ? bn / 2 : bn));
     else if (p.chunked_b) ok &= map_chunked(&p.tm_b, g.B, g.dtype, wb, g.K, b_count, g.ldb, g.b_stride);
     else ok &= map3(&p.tm_b, g.B, g.dtype, g.N, g.K, b_count, g.ldb, g.b_stride, BK);
     const int64_t c_count = g.group == GROUP_K ? g.groups : g.splits > 1 ? g.splits : 1;
@@ -756,7 +820,8 @@ cudaError_t train_gemm(const TrainGemm& g, int num_sms, cudaStream_t st) {
     p.M = static_cast<int32_t>(g.M);
     p.N = static_cast<int32_t>(g.N);
     p.K = static_cast<int32_t>(g.K);
-    p.tiles_n = static_cast<int32_t>((g.N + BN - 1) / BN);
+    p.sub_bytes = A_BYTES + static_cast<int32_t>(pair ? bn / 2 : bn) * BK * 2;
+    p.tiles_n = static_cast<int32_t>((g.N + bn - 1) / bn);
     p.tiles_m = static_cast<int32_t>((g.M + tile_m - 1) / tile_m);
     p.groups = static_cast<int32_t>(g.groups);
     p.group = g.group;
@@ -819,7 +884,7 @@ cudaError_t train_gemm(const TrainGemm& g, int num_sms, cudaStream_t st) {
 cudaError_t launch_split_sum(const float* parts, int64_t ld, int64_t stride, int splits, float alpha,
                              const float* alpha_dev, void* out, int64_t out_ld, int out_dtype, int64_t rows,
                              int64_t cols, int kind, int num_sms, cudaStream_t st) {
-    const int64_t blocks = (rows * cols + 255) / 256;
+    const int64_t blocks = (rows * (ld / 4) + 255) / 256;
     const dim3 grid(static_cast<unsigned>(blocks < num_sms * 8 ? blocks : num_sms * 8));
     launch_begin(kind, st);
     const cudaError_t e =
