@@ -148,6 +148,20 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
+// True in one lane of a converged warp.  Loops that the whole warp runs, with
+// only the issue behind this predicate, keep addresses and descriptors in
+// uniform registers; a loop that one lane runs alone moves them there for
+// each instruction.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(e));
+    return e != 0;
+}
+
 __device__ __forceinline__ void tc_fence_before() {
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
 }
@@ -170,6 +184,28 @@ __device__ __forceinline__ void tc_mma(uint32_t d_tmem, uint64_t adesc, uint64_t
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+
+// One staged k-block: four 16-deep MMAs whose descriptors are step_a and
+// step_b apart; the first adds to the accumulator only with `accumulate`.
+#define MUON_MMA_K_BLOCK(group)                                                            \
+    asm volatile(                                                                          \
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"                      \
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 q, 0, 0;\n\t"                                \
+        "add.s64 a1, %1, %5;\n\tadd.s64 a2, a1, %5;\n\tadd.s64 a3, a2, %5;\n\t"            \
+        "add.s64 b1, %2, %6;\n\tadd.s64 b2, b1, %6;\n\tadd.s64 b3, b2, %6;\n\t"            \
+        "tcgen05.mma.cta_group::" group ".kind::f16 [%0], %1, %2, %3, p;\n\t"              \
+        "tcgen05.mma.cta_group::" group ".kind::f16 [%0], a1, b1, %3, q;\n\t"              \
+        "tcgen05.mma.cta_group::" group ".kind::f16 [%0], a2, b2, %3, q;\n\t"              \
+        "tcgen05.mma.cta_group::" group ".kind::f16 [%0], a3, b3, %3, q;\n\t}" ::"r"(d),   \
+        "l"(da), "l"(db), "r"(idesc), "r"(accumulate), "l"(step_a), "l"(step_b)            \
+        : "memory")
+template <bool kPair>
+__device__ __forceinline__ void tc_mma_k_block(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc,
+                                               uint32_t accumulate, uint64_t step_a, uint64_t step_b) {
+    if constexpr (kPair) MUON_MMA_K_BLOCK("2");
+    else MUON_MMA_K_BLOCK("1");
+}
+#undef MUON_MMA_K_BLOCK
 
 // 32 lanes x 32 consecutive fp32 columns; the wait is in the same asm block
 // so no use of the registers can be scheduled before the data has landed.

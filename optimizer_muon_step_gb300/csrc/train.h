@@ -65,7 +65,8 @@ cudaError_t launch_embed_grad(const EmbedGrad& a, void* workspace, int num_sms, 
 // ---- matrix products (train_gemm.cu) ---------------------------------------
 // C[M][N] = alpha * A B in fp32 sums over 16-bit operands.  A is [M][K]
 // row-major, or [K][M] with a_mn; B is [N][K], or [K][N] with b_mn.
-//   GROUP_M  M = all tokens' rows: rows of group e use B + e * b_stride
+//   GROUP_M  N = all tokens: columns of group e use A + e * a_stride, and C is
+//            stored transposed, a row of M elements per token (16-bit C)
 //   GROUP_K  K = all tokens' rows: C + e * c_stride sums over group e's rows
 // with groups the ranges [offsets[e], offsets[e + 1]) of the token axis.
 enum { GROUP_NONE = 0, GROUP_M = 1, GROUP_K = 2 };
@@ -92,7 +93,7 @@ struct TrainGemm {
     void* C;
     int64_t lda, ldb, ldc;  // elements
     int64_t M, N, K;
-    int64_t b_stride, c_stride;  // elements, between groups (c_stride: or splits)
+    int64_t a_stride, c_stride;  // elements, between groups (c_stride: or splits)
     const void* offsets;
     void* group_maps;        // GROUP_K: train_gemm_group_bytes of the workspace, 64-byte aligned
     const float* alpha_dev;  // multiplies alpha when not null

@@ -507,30 +507,30 @@ muon_status_t muon_expert_matmul(const void* x, int64_t x_ld, const void* weight
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     uint8_t* at = ws + kHeaderBytes;
     TrainGemm g = {};
-    g.A = x;
-    g.lda = x_ld;
-    g.B = weight;
-    g.ldb = cols;
+    g.A = weight;
+    g.lda = cols;
+    g.B = x;
+    g.ldb = x_ld;
     cudaError_t e = cudaSuccess;
     if (!tma_ready(x, x_ld)) {
         e = launch_pack(x, x_ld, at, pitch8(xc), tokens, xc, num_sms, st);
-        g.A = at;
-        g.lda = pitch8(xc);
+        g.B = at;
+        g.ldb = pitch8(xc);
         at += packed_bytes(tokens, xc);
     }
     if (e == cudaSuccess && !tma_ready(weight, cols)) {
         e = launch_pack(weight, cols, at, pitch8(cols), experts * rows, cols, num_sms, st);
-        g.B = at;
-        g.ldb = pitch8(cols);
+        g.A = at;
+        g.lda = pitch8(cols);
     }
     if (e != cudaSuccess) return from_cuda(e);
-    g.b_mn = transpose != 0;
-    g.b_stride = rows * g.ldb;
+    g.a_mn = transpose != 0;
+    g.a_stride = rows * g.lda;
     g.C = y;
     g.ldc = y_ld;
     g.c_dtype = dtype;
-    g.M = tokens;
-    g.N = yc;
+    g.M = yc;
+    g.N = tokens;
     g.K = xc;
     g.group = GROUP_M;
     g.groups = experts;

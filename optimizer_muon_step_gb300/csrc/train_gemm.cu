@@ -6,18 +6,27 @@
 //   GROUP_M     rows [o_e, o_{e+1}) of A and C use B_e
 //   GROUP_K     C_e = sum over k in [o_e, o_{e+1})
 //
-// One persistent kernel of 6 warps per CTA (or CTA pair), with the roles of
+// One persistent kernel of 7 warps per CTA (or CTA pair), with the roles of
 // the Newton-Schulz kernel: warp 0 feeds a shared-memory ring by TMA, warp 1
 // issues tcgen05.mma into two 256-column TMEM accumulators, warps 2..5 empty
-// the other accumulator.  Either operand may be K-major or MN-major (the
+// the other accumulator; warp 6 works out the tiles.  Either operand may be K-major or MN-major (the
 // instruction descriptor's major bits), so gradients of the weights and the
 // inputs need no transposed copy.
 //
 // The groups' ranges are read from the device, so a call needs no host
-// synchronisation.  Each role finds its tiles by itself: the warp holds 32
-// groups' ranges at a time, one per lane, and walks the tile list in order.
-// GROUP_M tiles that reach past their group load the neighbour's rows and
-// store only their own.  GROUP_K must not see the neighbour's rows at all (0
+// synchronisation.  Warp 6 holds 256 groups' ranges at a time, eight per lane,
+// walks the tile list and hands the tiles to the other warps through a ring
+// in shared memory, several ahead: found by each warp for itself they cost
+// SCHEDNOTE.
+//
+// GROUP_M computes C_e^T = B_e A_e^T: the weights' rows lie along the MMA's M
+// (128 or 256, which they fill), the tokens along its N, which takes any
+// multiple of 16 or 32.  An expert's last tile thus costs what its tokens
+// cost, not a whole tile of 128 or 256 rows, and a decoding batch's few
+// tokens leave shared memory to the stream of weights.  Tiles that reach past
+// their group load the neighbour's rows and store only their own columns.
+//
+// GROUP_K must not see the neighbour's rows at all (0
 // times NaN is NaN): each group reads through its own copy of the tensor
 // maps whose row extent ends where the group does, so the TMA unit fills the
 // rest of the last k-block with zeros.
@@ -37,26 +46,24 @@ namespace {
 constexpr int BM = 128;   // rows of a CTA's tile
 constexpr int BN = 256;   // columns of a tile
 constexpr int BK = 64;    // one 128-byte swizzle row of 16-bit elements
-constexpr int A_BYTES = BM * BK * 2;
 constexpr int EPI_WARPS = 4;
-constexpr int NUM_THREADS = 64 + 32 * EPI_WARPS;
+constexpr int NUM_THREADS = 64 + 32 * EPI_WARPS + 32;
+constexpr int SCHED_WARP = 2 + EPI_WARPS;
+constexpr int TILE_SLOTS = 4;         // tiles handed on ahead
 constexpr int TMEM_COLS = 512;
 constexpr int EBUF_BYTES = 32 * 128;  // a block of 32 rows x 128 bytes on its way out
 constexpr int NSLOT = 2;              // blocks per epilogue warp
 constexpr int EBUFS_BYTES = EPI_WARPS * NSLOT * EBUF_BYTES;
 
-// Ring: pairs stage 128 rows of each operand per CTA, two k-blocks per
-// stage; single CTAs 128 and 256 rows, one k-block per stage.
-template <bool kPair>
-struct Ring {
-    static constexpr int B_ROWS = kPair ? BN / 2 : BN;
-    static constexpr int SUB_BYTES = A_BYTES + B_ROWS * BK * 2;
-    static constexpr int KPS = kPair ? 2 : 1;
-    static constexpr int STAGES = kPair ? 3 : 4;
-    static constexpr int STAGE_BYTES = KPS * SUB_BYTES;
-    static constexpr int TILE_M = kPair ? 2 * BM : BM;
-    static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EBUFS_BYTES + 512;
-};
+// The ring: stages of one k-block (two on pairs with full tiles, see
+// ns_gemm.cu), each this CTA's rows of A, then of B.  Narrow tiles take
+// smaller stages and more of them.
+constexpr int RING_BYTES = 196608;
+constexpr int MAX_STAGES = 12;
+constexpr int SMEM_BYTES = 1024 + RING_BYTES + EBUFS_BYTES + 1024;
+
+// What a product's tiles end in.
+enum { END_STORE = 0, END_CE = 1, END_TOKENS = 2 };
 
 struct GemmParams {
     CUtensorMap tm_a, tm_b, tm_c;
@@ -67,10 +74,12 @@ struct GemmParams {
     int* status;
     CeEpilogue ce;
     int64_t ldc, c_stride;          // elements
-    int32_t M, N, K;                // GROUP_M: M rows in all; GROUP_K: K rows in all
-    int32_t tiles_m, tiles_n, total_tiles;  // GROUP_M: tiles_m and total_tiles are found on the device
+    int32_t M, N, K;                // GROUP_M: N tokens in all; GROUP_K: K tokens in all
+    int32_t tiles_m, tiles_n, total_tiles;  // GROUP_M: tiles_n and total_tiles are found on the device
     int32_t bn;                     // columns of a tile, a multiple of 32 (64 for 16-bit C) up to BN
-    int32_t sub_bytes;              // of one staged k-block, this CTA's part
+    int32_t stages, kps;            // ring: stages, k-blocks in each
+    int32_t a_slot, b_slot;         // bytes of a k-block's parts in the ring
+    int32_t a_load;                 // bytes a copy of A brings
     int32_t band;                   // rows of tiles walked together (GROUP_NONE, GROUP_K)
     int32_t groups, group, offsets64;
     int32_t k_blocks;               // per split (GROUP_NONE)
@@ -84,10 +93,12 @@ struct GemmParams {
 struct Tile {
     int row0, rows_end;  // first row of the (pair) tile, end of its rows
     int col0, tn;        // first column, column tile
+    int cols_end;        // end of the columns to be stored
+    int n;               // columns the MMA computes
     int c2;              // third coordinate of C: group or split
     int group;           // weight matrix (GROUP_M), tensor maps (GROUP_K)
     int k0;              // first k (elements)
-    int nk;              // k-blocks
+    int nk;              // k-blocks; -1: no more tiles
 };
 
 __device__ __forceinline__ int clamped(const GemmParams& p, int e, int n) {
@@ -100,11 +111,23 @@ template <int TILE_M>
 struct Walker {
     const GemmParams& p;
     int lane;
-    // GROUP_M: the window of groups base - 1 .. base + 30 (lane l holds group
-    // base + l - 1; -1 and `groups` are the rows before and after all groups)
-    int base, first, total, lo, hi, incl;
+    // GROUP_M: a window of 32 * kPer groups from `base` on, lane l holding the
+    // kPer from base + l * kPer; groups -1 and p.groups are the tokens before
+    // and after all groups.  One window, so one round trip to memory, for up
+    // to 254 groups.
+    static constexpr int kPer = 8;
+    int base, first, total, incl;
+    int edge[kPer + 1];  // the lane's group i has tokens [edge[i], edge[i + 1])
 
-    __device__ Walker(const GemmParams& prm, int ln) : p(prm), lane(ln), base(-32), first(0), total(0), lo(0), hi(0), incl(0) {}
+    __device__ Walker(const GemmParams& prm, int ln) : p(prm), lane(ln), base(-1 - 32 * kPer), first(0), total(0), incl(0) {}
+
+    // where group e begins (groups + 1: where the tokens after all groups end)
+    __device__ int begin_of(int e) const { return e < 0 ? 0 : e > p.groups ? p.N : clamped(p, e, p.N); }
+
+    __device__ int tiles_of(int i) const {
+        const int n = edge[i + 1] - edge[i];
+        return n > 0 ? (n + p.bn - 1) / p.bn * p.tiles_m : 0;
+    }
 
     __device__ bool next(int t, Tile& o) {
         if (p.group != GROUP_M) {
@@ -122,6 +145,12 @@ struct Walker {
             o.rows_end = p.M;
             o.tn = n;
             o.col0 = n * p.bn;
+            o.cols_end = p.N;
+            // at the edge the next multiple of 16 columns (pairs 32, or 128
+            // where each half starts on a 64-column chunk)
+            const int rem = p.N - o.col0;
+            const int q = TILE_M == BM ? 15 : p.b_mn && p.chunked_b ? 127 : 31;
+            o.n = rem < p.bn ? (rem + q) & ~q : p.bn;
             o.c2 = o.group = s;
             if (p.group == GROUP_K) {
                 const int a = clamped(p, s, p.K), e = clamped(p, s + 1, p.K);
@@ -138,15 +167,13 @@ struct Walker {
         }
         while (t >= first + total) {
             first += total;
-            base += 32;
-            if (base > p.groups + 1) return false;
-            const int e = base + lane - 1;
-            lo = hi = 0;
-            if (e <= p.groups) {
-                lo = e < 0 ? 0 : clamped(p, e, p.M);
-                hi = e >= p.groups ? p.M : clamped(p, e + 1, p.M);
-            }
-            incl = hi > lo ? (hi - lo + TILE_M - 1) / TILE_M * p.tiles_n : 0;
+            base += 32 * kPer;
+            if (base > p.groups) return false;
+#pragma unroll
+            for (int i = 0; i <= kPer; ++i) edge[i] = begin_of(base + lane * kPer + i);
+            incl = 0;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) incl += tiles_of(i);
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int x = __shfl_up_sync(0xffffffffu, incl, d);
@@ -156,15 +183,39 @@ struct Walker {
         }
         const int src = __ffs(__ballot_sync(0xffffffffu, t - first < incl)) - 1;
         const int prev = __shfl_sync(0xffffffffu, incl, src > 0 ? src - 1 : 0);
-        const int a = __shfl_sync(0xffffffffu, lo, src), e = __shfl_sync(0xffffffffu, hi, src);
-        const int r = t - first - (src > 0 ? prev : 0);
-        const int tm = (e - a + TILE_M - 1) / TILE_M;
-        const int n = r / tm;
-        const int g = base + src - 1;
-        o.row0 = a + (r - n * tm) * TILE_M;
-        o.rows_end = e;
-        o.tn = n;
-        o.col0 = n * p.bn;
+        int r = t - first - (src > 0 ? prev : 0);
+        int a = 0, e = 0, at = 0;  // lane src finds the group among its own
+        bool found = false;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int n = tiles_of(i);
+            if (!found) {
+                if (r < n) {
+                    found = true;
+                    a = edge[i];
+                    e = edge[i + 1];
+                    at = i;
+                } else {
+                    r -= n;
+                }
+            }
+        }
+        r = __shfl_sync(0xffffffffu, r, src);
+        a = __shfl_sync(0xffffffffu, a, src);
+        e = __shfl_sync(0xffffffffu, e, src);
+        at = __shfl_sync(0xffffffffu, at, src);
+        const int tn = (e - a + p.bn - 1) / p.bn;
+        const int m = r / tn;
+        const int g = base + src * kPer + at;
+        // the group's tokens in tn tiles of equal width
+        constexpr int q = TILE_M == BM ? 15 : 31;
+        const int w = ((e - a + tn - 1) / tn + q) & ~q;
+        o.row0 = m * TILE_M;
+        o.rows_end = p.M;
+        o.tn = 0;
+        o.col0 = a + (r - m * tn) * w;
+        o.cols_end = o.col0 + w < e ? o.col0 + w : e;
+        o.n = w;
         o.c2 = 0;
         o.group = g;
         o.k0 = 0;
@@ -172,15 +223,6 @@ struct Walker {
         return true;
     }
 };
-
-// Columns the MMA computes: the tile's, or at the edge the next multiple of 32 (16
-// for single CTAs; of 128 with chunked pairs, whose halves start on a chunk).
-template <bool kPair>
-__device__ __forceinline__ int tile_cols(const GemmParams& p, int col0) {
-    const int rem = p.N - col0;
-    const int q = !kPair ? 15 : p.b_mn && p.chunked_b ? 127 : 31;
-    return rem < p.bn ? (rem + q) & ~q : p.bn;
-}
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -197,9 +239,8 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi, int dtype) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// The finished block in shared memory (32 rows of 128 bytes, swizzled) to C
-// with plain stores: rows of a group that ends inside the block, and C's that
-// no tensor map can describe.
+// The finished block in shared memory (32 rows of 128 bytes, swizzled) to a C
+// that no tensor map can describe, with plain stores.
 __device__ __forceinline__ void store_rows(const GemmParams& p, const uint8_t* buf, int row, int rows_end, int col,
                                            int c2, int lane) {
     const bool wide = p.c_dtype == MUON_F32;
@@ -269,19 +310,23 @@ __device__ __forceinline__ void write_scalars(const CeEpilogue& ce, int lane) {
     }
 }
 
-template <bool kPair, bool kCe>
+template <bool kPair, int kEnd>
 __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
-    typedef Ring<kPair> R;
+    constexpr bool kCe = kEnd == END_CE;
+    constexpr int TILE_M = kPair ? 2 * BM : BM;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* ebufs = smem + R::STAGES * R::STAGE_BYTES;
+    uint8_t* ebufs = smem + RING_BYTES;
     uint64_t* bars = reinterpret_cast<uint64_t*>(ebufs + EBUFS_BYTES);
     uint64_t* full_bar = bars;
-    uint64_t* empty_bar = bars + R::STAGES;
-    uint64_t* tfull_bar = bars + 2 * R::STAGES;
+    uint64_t* empty_bar = bars + MAX_STAGES;
+    uint64_t* tfull_bar = bars + 2 * MAX_STAGES;
     uint64_t* tempty_bar = tfull_bar + 2;
     uint64_t* drain_bar = tempty_bar + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
+    uint64_t* sfull_bar = drain_bar + 1;   // a tile in the slot
+    uint64_t* sempty_bar = sfull_bar + TILE_SLOTS;
+    Tile* tile_ring = reinterpret_cast<Tile*>(sempty_bar + TILE_SLOTS);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tile_ring + TILE_SLOTS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5;
@@ -291,7 +336,7 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
     const int workers = kPair ? gridDim.x >> 1 : gridDim.x;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < R::STAGES; ++s) {
+        for (int s = 0; s < p.stages; ++s) {
             mbar_init(smem_u32(&full_bar[s]), 1);
             mbar_init(smem_u32(&empty_bar[s]), 1);
         }
@@ -300,6 +345,11 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
             mbar_init(smem_u32(&tempty_bar[a]), (kPair ? 2 : 1) * EPI_WARPS);
         }
         mbar_init(smem_u32(drain_bar), 1);
+        for (int s = 0; s < TILE_SLOTS; ++s) {
+            mbar_init(smem_u32(&sfull_bar[s]), 1);
+            // readers: producer, epilogue warps, and the MMA issuer of the even CTA
+            mbar_init(smem_u32(&sempty_bar[s]), 1 + EPI_WARPS + (rank == 0 ? 1 : 0));
+        }
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -329,41 +379,73 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
     // seconds later
     if ((p.group == GROUP_M || (kCe && p.ce.first)) && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
 
-    Walker<R::TILE_M> walk(p, lane);
+    const int sub_slot = p.a_slot + p.b_slot;
+    const uint32_t ring0 = smem_u32(smem), full0 = smem_u32(full_bar), empty0 = smem_u32(empty_bar);
+    const uint32_t full_leader0 = kPair ? mapa_shared(full0, 0) : full0;
+    // The i-th tile of this CTA for one of its reading warps; false after the
+    // last one, or when aborting.
+    auto read_tile = [&](int i, Tile& tile) {
+        const int s = i % TILE_SLOTS;
+        if (!wait_bounded(smem_u32(&sfull_bar[s]), static_cast<uint32_t>(i / TILE_SLOTS) & 1u, abort_flag, p.status))
+            return false;
+        tile = tile_ring[s];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sempty_bar[s]));
+        return tile.nk >= 0;
+    };
     Tile tile;
-    if (warp == 0) {
+    if (warp == SCHED_WARP) {
+        // ---------------- tiles ----------------
+        Walker<TILE_M> walk(p, lane);
+        int i = 0;
+        for (int t = worker;; t += workers, ++i) {
+            const bool more = walk.next(t, tile);
+            const int s = i % TILE_SLOTS;
+            if (!wait_bounded(smem_u32(&sempty_bar[s]), (static_cast<uint32_t>(i / TILE_SLOTS) & 1u) ^ 1u, abort_flag,
+                              p.status))
+                break;
+            if (lane == 0) {
+                if (!more) tile.nk = -1;
+                tile_ring[s] = tile;
+                mbar_arrive(smem_u32(&sfull_bar[s]));
+            }
+            __syncwarp();
+            if (!more) break;
+        }
+    } else if (warp == 0) {
         // ---------------- TMA producer ----------------
         int stage = 0;
         uint32_t phase = 0;
-        int last_parity[R::STAGES];
-        for (int s = 0; s < R::STAGES; ++s) last_parity[s] = -1;
+        int issued = 0;  // stages filled
         bool ok = true;
-        int acquired = -1;  // GROUP_K: the group whose tensor maps this thread has acquired
-        for (int t = worker; ok && walk.next(t, tile); t += workers) {
-            if (lane == 0) {
-                const CUtensorMap* ma = &p.tm_a;
-                const CUtensorMap* mb = &p.tm_b;
-                if (p.group == GROUP_K) {
-                    ma = p.group_maps + 2 * tile.group;
-                    mb = ma + 1;
-                    if (acquired != tile.group && tile.nk > 0) {
-                        acquired = tile.group;
-                        asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(ma) : "memory");
-                        asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(mb) : "memory");
-                    }
+        int acquired = -1;  // GROUP_K: the group whose tensor maps have been acquired
+        const bool elected = elect_one();
+        for (int i = 0; ok && read_tile(i, tile); ++i) {
+            const CUtensorMap* ma = &p.tm_a;
+            const CUtensorMap* mb = &p.tm_b;
+            if (p.group == GROUP_K) {
+                ma = p.group_maps + 2 * tile.group;
+                mb = ma + 1;
+                if (elected && tile.nk > 0 && tile.group != acquired) {
+                    asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(ma) : "memory");
+                    asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(mb) : "memory");
                 }
-                const int row = tile.row0 + rank * BM;
-                const int b0 = tile.col0 + (kPair ? rank * (tile_cols<kPair>(p, tile.col0) / 2) : 0);
-                const int b2 = p.group == GROUP_M ? tile.group : 0;
-                for (int kb0 = 0; kb0 < tile.nk; kb0 += R::KPS) {
-                    if (!wait_bounded(smem_u32(&empty_bar[stage]), phase ^ 1u, abort_flag, p.status)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t fb = smem_u32(&full_bar[stage]);
-                    const uint32_t fl = kPair ? mapa_shared(fb, 0) : fb;
-                    const int nsub = tile.nk - kb0 < R::KPS ? tile.nk - kb0 : R::KPS;
-                    if (rank == 0) mbar_expect_tx(fb, (kPair ? 2 : 1) * p.sub_bytes * nsub);
+                acquired = tile.group;
+            }
+            const int row = tile.row0 + rank * BM;
+            const int half = kPair ? tile.n / 2 : tile.n;  // columns this CTA stages
+            const int b0 = tile.col0 + rank * half;
+            const int a2 = p.group == GROUP_M ? tile.group : 0;
+            const uint32_t tx = static_cast<uint32_t>((kPair ? 2 : 1) * (p.a_load + p.b_slot));
+            for (int kb0 = 0; kb0 < tile.nk; kb0 += p.kps) {
+                if (!wait_bounded(empty0 + 8 * stage, phase ^ 1u, abort_flag, p.status)) {
+                    ok = false;
+                    break;
+                }
+                if (elected) {
+                    const uint32_t fl = full_leader0 + 8 * stage;
+                    const int nsub = tile.nk - kb0 < p.kps ? tile.nk - kb0 : p.kps;
+                    if (rank == 0) mbar_expect_tx(full0 + 8 * stage, tx * nsub);
                     auto load3 = [&](uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2) {
                         if (kPair) tma_load_3d_pair(dst, map, c0, c1, c2, fl);
                         else tma_load_3d(dst, map, c0, c1, c2, fl);
@@ -380,88 +462,86 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
                                 load3(dst + static_cast<uint32_t>(c) * MN_CHUNK_BYTES, map, r0 + 64 * c, k, c2);
                         }
                     };
-                    for (int q = 0; q < nsub; ++q) {
-                        const int k = tile.k0 + (kb0 + q) * BK;
-                        const uint32_t sa = smem_u32(smem + stage * R::STAGE_BYTES + q * R::SUB_BYTES);
-                        const uint32_t sb = sa + A_BYTES;
-                        if (p.a_mn) load_mn(sa, ma, p.chunked_a, row, BM / 64, k, 0);
-                        else load3(sa, ma, k, row, 0);
-                        if (p.b_mn) load_mn(sb, mb, p.chunked_b, b0, R::B_ROWS / 64, k, b2);
-                        else load3(sb, mb, k, b0, b2);
-                    }
-                    last_parity[stage] = static_cast<int>(phase);
-                    if (++stage == R::STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
+                    uint32_t sa = ring0 + static_cast<uint32_t>(stage * p.kps * sub_slot);
+                    int k = tile.k0 + kb0 * BK;
+                    for (int q = 0; q < nsub; ++q, sa += sub_slot, k += BK) {
+                        const uint32_t sb = sa + p.a_slot;
+                        if (p.a_mn) load_mn(sa, ma, p.chunked_a, row, BM / 64, k, a2);
+                        else load3(sa, ma, k, row, a2);
+                        if (p.b_mn) load_mn(sb, mb, p.chunked_b, b0, (kPair ? BN / 2 : BN) / 64, k, 0);
+                        else load3(sb, mb, k, b0, 0);
                     }
                 }
+                ++issued;
+                if (++stage == p.stages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
             }
-            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         }
         // drain: every issued copy must land before the CTA may exit (the even
         // CTA's full barriers count both CTAs' copies)
-        if (lane == 0 && rank == 0)
-            for (int s = 0; s < R::STAGES; ++s)
-                if (last_parity[s] >= 0) wait_drain(smem_u32(&full_bar[s]), static_cast<uint32_t>(last_parity[s]));
-        __syncwarp();
+        if (rank == 0)
+            for (int s = 0; s < p.stages && s < issued; ++s)
+                wait_drain(smem_u32(&full_bar[s]), static_cast<uint32_t>((issued - 1 - s) / p.stages) & 1u);
     } else if (warp == 1 && rank == 0) {
         // ---------------- MMA issuer ----------------
         int stage = 0;
         uint32_t phase = 0;
         int local = 0;
         bool ok = true;
-        for (int t = worker; ok && walk.next(t, tile); t += workers) {
+        const bool elected = elect_one();
+        // descriptors of the ring's first k-block; others differ in the address
+        // field alone (16-byte units, below 2^14 for all of shared memory)
+        const uint64_t desc_a = operand_desc(ring0, 0, p.a_mn), desc_b = operand_desc(ring0 + p.a_slot, 0, p.b_mn);
+        const uint64_t step_a = p.a_mn ? 16 * 128 / 16 : 32 / 16, step_b = p.b_mn ? 16 * 128 / 16 : 32 / 16;
+        for (int i = 0; ok && read_tile(i, tile); ++i) {
             if (tile.nk == 0) continue;
-            if (lane == 0) {
-                const int acc = local & 1;
-                const uint32_t acc_phase = static_cast<uint32_t>(local >> 1) & 1u;
-                ok = wait_bounded(smem_u32(&tempty_bar[acc]), acc_phase ^ 1u, abort_flag, p.status);
-                tc_fence_after();
-                const int n = tile_cols<kPair>(p, tile.col0);
-                const uint32_t idesc = p.idesc | (static_cast<uint32_t>(n >> 3) << 17) |
-                                       (static_cast<uint32_t>(R::TILE_M >> 4) << 24);
-                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
-                for (int kb0 = 0; ok && kb0 < tile.nk; kb0 += R::KPS) {
-                    if (!wait_bounded(smem_u32(&full_bar[stage]), phase, abort_flag, p.status)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const int nsub = tile.nk - kb0 < R::KPS ? tile.nk - kb0 : R::KPS;
-                    for (int q = 0; q < nsub; ++q) {
-                        const uint32_t sa = smem_u32(smem + stage * R::STAGE_BYTES + q * R::SUB_BYTES);
-                        const uint32_t sb = sa + A_BYTES;
-#pragma unroll
-                        for (int k = 0; k < BK / 16; ++k) {
-                            const uint64_t da = operand_desc(sa, k, p.a_mn), db = operand_desc(sb, k, p.b_mn);
-                            const uint32_t more = (kb0 | q | k) != 0 ? 1u : 0u;
-                            if (kPair) tc_mma_pair(d_tmem, da, db, idesc, more);
-                            else tc_mma(d_tmem, da, db, idesc, more);
-                        }
-                    }
-                    if (kPair) tc_commit_pair_mc(smem_u32(&empty_bar[stage]), 0x3);
-                    else tc_commit(smem_u32(&empty_bar[stage]));
-                    if (++stage == R::STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+            const int acc = local & 1;
+            const uint32_t acc_phase = static_cast<uint32_t>(local >> 1) & 1u;
+            ok = wait_bounded(smem_u32(&tempty_bar[acc]), acc_phase ^ 1u, abort_flag, p.status);
+            tc_fence_after();
+            const uint32_t idesc = p.idesc | (static_cast<uint32_t>(tile.n >> 3) << 17) |
+                                   (static_cast<uint32_t>(TILE_M >> 4) << 24);
+            const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
+            uint32_t more = 0;  // the tile's first MMA overwrites the accumulator
+            for (int kb0 = 0; ok && kb0 < tile.nk; kb0 += p.kps) {
+                if (!wait_bounded(full0 + 8 * stage, phase, abort_flag, p.status)) {
+                    ok = false;
+                    break;
                 }
-                if (ok) {
-                    if (kPair) tc_commit_pair_mc(smem_u32(&tfull_bar[acc]), 0x3);
-                    else tc_commit(smem_u32(&tfull_bar[acc]));
+                tc_fence_after();
+                const int nsub = tile.nk - kb0 < p.kps ? tile.nk - kb0 : p.kps;
+                uint32_t at = static_cast<uint32_t>(stage * p.kps * sub_slot) >> 4;
+                for (int q = 0; q < nsub; ++q, at += static_cast<uint32_t>(sub_slot) >> 4) {
+                    if (elected) tc_mma_k_block<kPair>(d_tmem, desc_a + at, desc_b + at, idesc, more, step_a, step_b);
+                    more = 1;
+                }
+                if (elected) {
+                    if (kPair) tc_commit_pair_mc(empty0 + 8 * stage, 0x3);
+                    else tc_commit(empty0 + 8 * stage);
+                }
+                if (++stage == p.stages) {
+                    stage = 0;
+                    phase ^= 1u;
                 }
             }
+            if (ok && elected) {
+                if (kPair) tc_commit_pair_mc(smem_u32(&tfull_bar[acc]), 0x3);
+                else tc_commit(smem_u32(&tfull_bar[acc]));
+            }
             ++local;
-            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         }
         // drain: all issued MMAs complete before TMEM is released
-        if (lane == 0) {
+        if (elected) {
             if (kPair) tc_commit_pair_mc(smem_u32(drain_bar), 0x1);
             else tc_commit(smem_u32(drain_bar));
-            wait_drain(smem_u32(drain_bar), 0);
         }
-        __syncwarp();
-    } else if (warp >= 2) {
+        wait_drain(smem_u32(drain_bar), 0);
+    } else if (warp == 1) {
+        // the odd CTA's second warp has no part in the product
+        if (kCe && kPair && p.ce.first && blockIdx.x == 1) write_scalars(p.ce, lane);
+    } else {
         // ---------------- epilogue ----------------
         const int quarter = warp & 3;  // TMEM lanes 32 * quarter .. + 31
         const int ew = warp - 2;
@@ -470,8 +550,8 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
         int local = 0;
         const float alpha = p.alpha_dev ? p.alpha * *p.alpha_dev : p.alpha;
         const int cols = p.c_dtype == MUON_F32 ? 32 : 64;
-        if (kCe && p.ce.first && blockIdx.x == 0 && ew == 0) write_scalars(p.ce, lane);
-        for (int t = worker; walk.next(t, tile); t += workers) {
+        if (kCe && !kPair && p.ce.first && blockIdx.x == 0 && ew == 0) write_scalars(p.ce, lane);
+        for (int i = 0; read_tile(i, tile); ++i) {
             const int acc = local & 1;
             const uint32_t acc_phase = static_cast<uint32_t>(local >> 1) & 1u;
             const int row = tile.row0 + rank * BM + quarter * 32;
@@ -483,8 +563,51 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
             }
             const uint32_t t_addr = tmem_base + static_cast<uint32_t>(acc * BN) + (static_cast<uint32_t>(quarter * 32) << 16);
             // an empty group adds nothing
-            const bool mine = row < tile.rows_end && (live || !p.accumulate);
-            const bool by_tma = p.tma_c && (p.group != GROUP_M || row + 32 <= tile.rows_end);
+            const bool mine = kEnd != END_TOKENS && row < tile.rows_end && (live || !p.accumulate);
+            const bool by_tma = p.tma_c;
+            if (kEnd == END_TOKENS && row < tile.rows_end) {
+                // 32 tokens at a time, transposed through shared memory: the
+                // lanes (features) write side by side into each token's 64
+                // bytes, and a tensor store takes the block to C.  A group's
+                // last tokens are stored one by one.
+                const int cols = tile.cols_end - tile.col0;
+                uint16_t* out = static_cast<uint16_t*>(p.C) + row + lane;
+                for (int c = 0; c < cols; c += 32) {
+                    float v[32];
+                    if (live) {
+                        tmem_load_32cols(t_addr + static_cast<uint32_t>(c), v);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = 0.f;
+                    }
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) w[i] = pack16(v[2 * i], v[2 * i + 1], p.c_dtype);
+                    if (by_tma && c + 32 <= cols) {
+                        uint8_t* buf = slots + (seq % NSLOT) * EBUF_BYTES;
+                        if (lane == 0) bulk_wait_read<NSLOT - 1>();
+                        __syncwarp();
+                        uint16_t* b = reinterpret_cast<uint16_t*>(buf) + lane;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            b[64 * i] = static_cast<uint16_t>(w[i]);
+                            b[64 * i + 32] = static_cast<uint16_t>(w[i] >> 16);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_3d(&p.tm_c, smem_u32(buf), row, tile.col0 + c, 0);
+                            bulk_commit();
+                        }
+                        ++seq;
+                    } else if (row + lane < tile.rows_end) {
+                        uint16_t* o = out + static_cast<int64_t>(tile.col0 + c) * p.ldc;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i, o += p.ldc)
+                            if (c + i < cols) *o = static_cast<uint16_t>(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
+                    }
+                }
+            }
             RowSums rs = {-INFINITY, 0.f};
             int target = -1;
             if (kCe && mine && row + lane < p.M) {
@@ -597,15 +720,15 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
     }
 }
 
-template <bool kCe>
+template <int kEnd>
 __global__ void __launch_bounds__(NUM_THREADS, 1) train_gemm_kernel(const __grid_constant__ GemmParams p) {
-    train_gemm_body<false, kCe>(p);
+    train_gemm_body<false, kEnd>(p);
 }
 
-template <bool kCe>
+template <int kEnd>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     train_gemm_pair_kernel(const __grid_constant__ GemmParams p) {
-    train_gemm_body<true, kCe>(p);
+    train_gemm_body<true, kEnd>(p);
 }
 
 // GROUP_K: a copy of A's and B's tensor map for every group, its row extent
@@ -689,6 +812,19 @@ bool map3(CUtensorMap* map, const void* base, int dtype, int64_t inner, int64_t 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// [rows][inner] of 16-bit elements in plain blocks of 32 x 32.
+bool map_block(CUtensorMap* map, const void* base, int dtype, int64_t inner, int64_t rows, int64_t ld) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows), 1};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * 2), static_cast<cuuint64_t>(rows * ld * 2)};
+    cuuint32_t box[3] = {32, 32, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, map_type(dtype), 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // The same matrices as [count][inner / 64][rows][64], two 64-wide chunks of
 // 64 rows a copy: MN-major operands whose width is a multiple of 64.
 bool map_chunked(CUtensorMap* map, const void* base, int dtype, int64_t inner, int64_t rows, int64_t count, int64_t ld,
@@ -706,6 +842,18 @@ bool map_chunked(CUtensorMap* map, const void* base, int dtype, int64_t inner, i
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+typedef void (*GemmKernel)(const GemmParams);
+
+GemmKernel single_kernel(int end) {
+    return end == END_CE ? train_gemm_kernel<END_CE> : end == END_TOKENS ? train_gemm_kernel<END_TOKENS> : train_gemm_kernel<END_STORE>;
+}
+
+GemmKernel pair_kernel(int end) {
+    return end == END_CE       ? train_gemm_pair_kernel<END_CE>
+           : end == END_TOKENS ? train_gemm_pair_kernel<END_TOKENS>
+                               : train_gemm_pair_kernel<END_STORE>;
+}
+
 // Kernel attributes and the pair occupancy, set up once per device (with
 // that device current) and remembered.
 cudaError_t setup(int* max_pairs) {
@@ -721,16 +869,17 @@ cudaError_t setup(int* max_pairs) {
     std::lock_guard<std::mutex> lock(mu);
     if (!done[dev]) {
         const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-        cudaError_t e = cudaFuncSetAttribute(train_gemm_kernel<false>, attr, Ring<false>::SMEM_BYTES);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(train_gemm_kernel<true>, attr, Ring<false>::SMEM_BYTES);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(train_gemm_pair_kernel<false>, attr, Ring<true>::SMEM_BYTES);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(train_gemm_pair_kernel<true>, attr, Ring<true>::SMEM_BYTES);
+        cudaError_t e = cudaSuccess;
+        for (int end = END_STORE; end <= END_TOKENS && e == cudaSuccess; ++end) {
+            e = cudaFuncSetAttribute(single_kernel(end), attr, SMEM_BYTES);
+            if (e == cudaSuccess) e = cudaFuncSetAttribute(pair_kernel(end), attr, SMEM_BYTES);
+        }
         if (e == cudaSuccess) {
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(2, 1, 1);
             cfg.blockDim = dim3(NUM_THREADS, 1, 1);
-            cfg.dynamicSmemBytes = Ring<true>::SMEM_BYTES;
-            e = cudaOccupancyMaxActiveClusters(&pairs[dev], train_gemm_pair_kernel<false>, &cfg);
+            cfg.dynamicSmemBytes = SMEM_BYTES;
+            e = cudaOccupancyMaxActiveClusters(&pairs[dev], pair_kernel(END_STORE), &cfg);
         }
         err[dev] = e;
         done[dev] = true;
@@ -741,7 +890,7 @@ cudaError_t setup(int* max_pairs) {
 
 // Pairs halve each SM's operand traffic but work on 256 rows at a time.
 bool use_pairs(const TrainGemm& g) {
-    if (g.group == GROUP_M) return g.M >= g.groups * 256;
+    if (g.group == GROUP_M) return g.M > BM && g.N >= g.groups * 128;
     return g.M > BM;
 }
 
@@ -757,11 +906,14 @@ size_t train_gemm_group_bytes(int64_t groups) { return static_cast<size_t>(group
 // Columns of a plain product's tiles when B is K-major: the width whose tiles
 // fill the last wave of CTAs best.  16 rows against 163840 columns: 224
 // columns leave 732 tiles for 152 CTAs (4.8 waves) where 256 leave 640 (4.2).
+// With more than 128 rows the product is bound by the MMAs, and narrower tiles
+// lose more by their edges than the last wave costs (999 x 32003, K = 1000: 79
+// us at 192 columns, 67 at 256).
 int64_t train_gemm_bn(int64_t M, int64_t N) {
-    const int64_t workers = M > BM ? 76 : 152, tm = M > BM ? 2 * BM : BM, rows = (M + tm - 1) / tm;
+    if (M > BM) return BN;
     int64_t best = BN, cost = 0;
     for (int64_t bn = BN; bn >= 128; bn -= 32) {
-        const int64_t waves = (rows * ((N + bn - 1) / bn) + workers - 1) / workers;
+        const int64_t waves = ((N + bn - 1) / bn + 151) / 152;
         const int64_t c = waves * (bn + 16);
         if (bn == BN || c < cost) {
             best = bn;
@@ -785,9 +937,25 @@ cudaError_t train_gemm(const TrainGemm& g, int num_sms, cudaStream_t st) {
     const bool pair = use_pairs(g);
     GemmParams p;
     memset(&p, 0, sizeof p);
-    const int64_t b_count = g.group == GROUP_M ? g.groups : 1;
-    const int64_t bn = g.ce.sums ? train_gemm_bn(g.M, g.N) : BN;
+    const int end = g.ce.sums ? END_CE : g.group == GROUP_M ? END_TOKENS : END_STORE;
+    const int64_t a_count = g.group == GROUP_M ? g.groups : 1;
+    int64_t bn = BN;
+    if (end == END_CE) {
+        bn = train_gemm_bn(g.M, g.N);
+    } else if (end == END_TOKENS) {
+        // about the tokens of two average experts, so that few experts need two tiles
+        const int64_t want = 2 * ((g.N + g.groups - 1) / g.groups);
+        bn = pair || want > 128 ? 256 : want > 64 ? 128 : want > 32 ? 64 : 32;
+    }
     p.bn = static_cast<int32_t>(bn);
+    // A's rows past a short product's are neither loaded nor stored: the MMA
+    // reads what the ring holds there
+    const int32_t a_rows = !g.a_mn && g.group == GROUP_NONE && g.M < BM ? static_cast<int32_t>(round_up(g.M, 8)) : BM;
+    p.a_slot = p.a_load = a_rows * BK * 2;
+    p.b_slot = static_cast<int32_t>(pair ? bn / 2 : bn) * BK * 2;
+    p.kps = pair ? 2 : 1;
+    p.stages = RING_BYTES / (p.kps * (p.a_slot + p.b_slot));
+    if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
     bool ok = true;
     // the widths of MN-major operands are rounded up where the row pitch
     // allows it: what lies past them enters only rows or columns of C that
@@ -796,18 +964,18 @@ cudaError_t train_gemm(const TrainGemm& g, int num_sms, cudaStream_t st) {
     const int64_t wb = g.b_mn && g.ldb >= round_up(g.N, 64) && g.b_padded ? round_up(g.N, 64) : g.N;
     p.chunked_a = g.a_mn && wa % 64 == 0;
     p.chunked_b = g.b_mn && wb % 64 == 0;
-    if (!g.a_mn) ok &= map3(&p.tm_a, g.A, g.dtype, g.K, g.M, 1, g.lda, 0, BM);
-    else if (p.chunked_a) ok &= map_chunked(&p.tm_a, g.A, g.dtype, wa, g.K, 1, g.lda, 0);
-    else ok &= map3(&p.tm_a, g.A, g.dtype, g.M, g.K, 1, g.lda, 0, BK);
-    if (!g.b_mn) ok &= map3(&p.tm_b, g.B, g.dtype, g.K, g.N, b_count, g.ldb, g.b_stride,
-                            static_cast<uint32_t>(pair ? bn / 2 : bn));
-    else if (p.chunked_b) ok &= map_chunked(&p.tm_b, g.B, g.dtype, wb, g.K, b_count, g.ldb, g.b_stride);
-    else ok &= map3(&p.tm_b, g.B, g.dtype, g.N, g.K, b_count, g.ldb, g.b_stride, BK);
+    if (!g.a_mn) ok &= map3(&p.tm_a, g.A, g.dtype, g.K, g.M, a_count, g.lda, g.a_stride, static_cast<uint32_t>(a_rows));
+    else if (p.chunked_a) ok &= map_chunked(&p.tm_a, g.A, g.dtype, wa, g.K, a_count, g.lda, g.a_stride);
+    else ok &= map3(&p.tm_a, g.A, g.dtype, g.M, g.K, a_count, g.lda, g.a_stride, BK);
+    if (!g.b_mn) ok &= map3(&p.tm_b, g.B, g.dtype, g.K, g.N, 1, g.ldb, 0, static_cast<uint32_t>(pair ? bn / 2 : bn));
+    else if (p.chunked_b) ok &= map_chunked(&p.tm_b, g.B, g.dtype, wb, g.K, 1, g.ldb, 0);
+    else ok &= map3(&p.tm_b, g.B, g.dtype, g.N, g.K, 1, g.ldb, 0, BK);
     const int64_t c_count = g.group == GROUP_K ? g.groups : g.splits > 1 ? g.splits : 1;
     const int64_t ce = static_cast<int64_t>(dtype_bytes(g.c_dtype));
     p.tma_c = g.C && (reinterpret_cast<uintptr_t>(g.C) & 15) == 0 && g.ldc * ce % 16 == 0 &&
               (c_count <= 1 || g.c_stride * ce % 16 == 0);
-    if (p.tma_c) ok &= map3(&p.tm_c, g.C, g.c_dtype, g.N, g.M, c_count, g.ldc, g.c_stride, 32);
+    if (p.tma_c && end == END_TOKENS) ok &= map_block(&p.tm_c, g.C, g.c_dtype, g.M, g.N, g.ldc);
+    else if (p.tma_c) ok &= map3(&p.tm_c, g.C, g.c_dtype, g.N, g.M, c_count, g.ldc, g.c_stride, 32);
     if (!ok) return cudaErrorInvalidValue;
     const int tile_m = pair ? 2 * BM : BM;
     p.offsets = g.offsets;
@@ -820,7 +988,6 @@ cudaError_t train_gemm(const TrainGemm& g, int num_sms, cudaStream_t st) {
     p.M = static_cast<int32_t>(g.M);
     p.N = static_cast<int32_t>(g.N);
     p.K = static_cast<int32_t>(g.K);
-    p.sub_bytes = A_BYTES + static_cast<int32_t>(pair ? bn / 2 : bn) * BK * 2;
     p.tiles_n = static_cast<int32_t>((g.N + bn - 1) / bn);
     p.tiles_m = static_cast<int32_t>((g.M + tile_m - 1) / tile_m);
     p.groups = static_cast<int32_t>(g.groups);
@@ -836,7 +1003,7 @@ cudaError_t train_gemm(const TrainGemm& g, int num_sms, cudaStream_t st) {
     const int64_t kb = (g.K + BK - 1) / BK;
     int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
     if (g.group == GROUP_M) {
-        tiles += (g.groups + 2) * static_cast<int64_t>(p.tiles_n);  // a bound: each group may end inside a tile
+        tiles += (g.groups + 2) * static_cast<int64_t>(p.tiles_m);  // a bound: each group may end inside a tile
     } else if (g.group == GROUP_K) {
         tiles *= g.groups;
     } else {
@@ -870,12 +1037,10 @@ cudaError_t train_gemm(const TrainGemm& g, int num_sms, cudaStream_t st) {
     if (pair) {
         int64_t n = max_pairs > 0 ? max_pairs : num_sms / 2;
         if (tiles < n) n = tiles;
-        e = launch_pdl(g.ce.sums ? train_gemm_pair_kernel<true> : train_gemm_pair_kernel<false>,
-                       dim3(static_cast<unsigned>(2 * n)), dim3(NUM_THREADS), Ring<true>::SMEM_BYTES, st, p);
+        e = launch_pdl(pair_kernel(end), dim3(static_cast<unsigned>(2 * n)), dim3(NUM_THREADS), SMEM_BYTES, st, p);
     } else {
         const int64_t n = tiles < num_sms ? tiles : num_sms;
-        e = launch_pdl(g.ce.sums ? train_gemm_kernel<true> : train_gemm_kernel<false>, dim3(static_cast<unsigned>(n)),
-                       dim3(NUM_THREADS), Ring<false>::SMEM_BYTES, st, p);
+        e = launch_pdl(single_kernel(end), dim3(static_cast<unsigned>(n)), dim3(NUM_THREADS), SMEM_BYTES, st, p);
     }
     launch_end(g.kind, st);
     return e == cudaSuccess ? cudaGetLastError() : e;
