@@ -59,7 +59,7 @@ __device__ __forceinline__ Row find_row(const CeBlock& b, int64_t t) {
     r.inside = r.target >= 0 && r.target < b.vocab;
     r.live = r.inside && r.target != b.ignore_index;
     float2 acc = make_float2(-INFINITY, 0.f);
-    for (int64_t i = threadIdx.x; i < b.col_tiles; i += kThreads) acc = join(acc, b.sums[t * b.col_tiles + i]);
+    for (int64_t i = threadIdx.x; i < b.row_sums; i += kThreads) acc = join(acc, b.sums[t * b.row_sums + i]);
     float s = 0.f;
     if (r.inside) {
         const T* h = static_cast<const T*>(b.hidden) + t * b.hidden_ld;

@@ -71,11 +71,11 @@ cudaError_t launch_embed_grad(const EmbedGrad& a, void* workspace, int num_sms, 
 // with groups the ranges [offsets[e], offsets[e + 1]) of the token axis.
 enum { GROUP_NONE = 0, GROUP_M = 1, GROUP_K = 2 };
 
-// Softmax sums of the product's rows, one pair per row and column tile:
-// (top, sum over the tile of exp2(x - top)), x = scale2 * product, without
+// Softmax sums of the product's rows, two pairs per row and column tile:
+// (top, sum over half the tile of exp2(x - top)), x = scale2 * product, without
 // the row's target column.  The product itself is stored when `store` is set.
 struct CeEpilogue {
-    float2* sums;         // [M][column tile]; null: no softmax
+    float2* sums;         // [M][column tile][half]; null: no softmax
     const void* targets;
     int32_t targets64;
     int32_t store;
@@ -113,8 +113,8 @@ struct TrainGemm {
 };
 cudaError_t train_gemm(const TrainGemm& g, int num_sms, cudaStream_t st);
 size_t train_gemm_group_bytes(int64_t groups);
-int64_t train_gemm_col_tiles(int64_t M, int64_t N);  // column tiles of a plain product with K-major B
-int64_t train_gemm_max_col_tiles(int64_t N);         // whatever M is
+int64_t train_gemm_sums(int64_t M, int64_t N);     // softmax sums per row: two per column tile
+int64_t train_gemm_max_sums(int64_t N);            // whatever M is
 int64_t train_gemm_tiles(int64_t M, int64_t N);    // tiles of a plain product, one per CTA or CTA pair
 // out = alpha * the sum of `splits` fp32 matrices, in order.
 cudaError_t launch_split_sum(const float* parts, int64_t ld, int64_t stride, int splits, float alpha,
@@ -133,14 +133,14 @@ struct CeBlock {
     const void* targets;
     const float* row_scale;  // may be null
     const float* scalars;    // see CeEpilogue
-    const float2* sums;      // [tokens][column tile], see CeEpilogue
+    const float2* sums;      // [tokens][row_sums], see CeEpilogue
     float* loss;
     float* lse;
     float* Z;                // logits; turned in place into the gradient's 16-bit rows
     void* packed;            // copy of the hidden rows for d_weight, zeros for ignored tokens
     int* status;
     int64_t hidden_ld, weight_ld, packed_ld, z_ld;
-    int64_t tokens, vocab, dim, ignore_index, col_tiles;
+    int64_t tokens, vocab, dim, ignore_index, row_sums;
     int32_t targets64, dtype;
     float logit_scale;
 };

@@ -231,7 +231,7 @@ size_t ce_total(const muon_linear_ce_t* p, bool grad, int64_t block, CeLayout* L
     size_t at = kFixedBytes;
     L->w_off = take(at, L->pack_w ? 2 * v * L->w_ld : 0);
     L->sum_off = take(at, L->sums ? 4 * v * d : 0);
-    L->tile_off = take(at, 8 * block * train_gemm_max_col_tiles(v));
+    L->tile_off = take(at, 8 * block * train_gemm_max_sums(v));
     L->h_off = take(at, grad || L->pack_h ? 2 * block * L->h_ld : 0);
     L->z_off = take(at, grad ? 4 * block * L->z_ld : 0);
     L->part_off = take(at, L->splits > 1 ? 4 * L->splits * block * L->part_ld : 0);
@@ -337,7 +337,7 @@ muon_status_t ce_run(const muon_linear_ce_t* p, bool grad, void* workspace, size
         c.vocab = v;
         c.dim = d;
         c.ignore_index = p->ignore_index;
-        c.col_tiles = train_gemm_col_tiles(m, v);
+        c.row_sums = train_gemm_sums(m, v);
         c.targets64 = p->targets_dtype == MUON_I64;
         c.dtype = p->dtype;
         c.logit_scale = p->logit_scale;

@@ -6,15 +6,16 @@
 //   GROUP_M     rows [o_e, o_{e+1}) of A and C use B_e
 //   GROUP_K     C_e = sum over k in [o_e, o_{e+1})
 //
-// One persistent kernel of 7 warps per CTA (or CTA pair), with the roles of
+// One persistent kernel of 11 warps per CTA (or CTA pair), with the roles of
 // the Newton-Schulz kernel: warp 0 feeds a shared-memory ring by TMA, warp 1
-// issues tcgen05.mma into two 256-column TMEM accumulators, warps 2..5 empty
-// the other accumulator; warp 6 works out the tiles.  Either operand may be K-major or MN-major (the
+// issues tcgen05.mma into two 256-column TMEM accumulators, warps 2..9 empty
+// the other accumulator, two for each quarter of its lanes; warp 10 works out
+// the tiles.  Either operand may be K-major or MN-major (the
 // instruction descriptor's major bits), so gradients of the weights and the
 // inputs need no transposed copy.
 //
 // The groups' ranges are read from the device, so a call needs no host
-// synchronisation.  Warp 6 holds 256 groups' ranges at a time, eight per lane,
+// synchronisation.  Warp 10 holds 256 groups' ranges at a time, eight per lane,
 // walks the tile list and hands the tiles to the other warps through a ring
 // in shared memory, several ahead: found by each warp for itself they cost
 // SCHEDNOTE.
@@ -46,18 +47,16 @@ namespace {
 constexpr int BM = 128;   // rows of a CTA's tile
 constexpr int BN = 256;   // columns of a tile
 constexpr int BK = 64;    // one 128-byte swizzle row of 16-bit elements
-constexpr int EPI_WARPS = 4;
+constexpr int EPI_WARPS = 8;  // with four, tiles of a few hundred k waited for their epilogues
 constexpr int NUM_THREADS = 64 + 32 * EPI_WARPS + 32;
 constexpr int SCHED_WARP = 2 + EPI_WARPS;
 constexpr int TILE_SLOTS = 4;         // tiles handed on ahead
 constexpr int TMEM_COLS = 512;
 constexpr int EBUF_BYTES = 32 * 128;  // a block of 32 rows x 128 bytes on its way out
-constexpr int NSLOT = 2;              // blocks per epilogue warp
-constexpr int EBUFS_BYTES = EPI_WARPS * NSLOT * EBUF_BYTES;
+constexpr int EBUFS_BYTES = EPI_WARPS * EBUF_BYTES;  // one per epilogue warp
 
-// The ring: stages of one k-block (two on pairs with full tiles, see
-// ns_gemm.cu), each this CTA's rows of A, then of B.  Narrow tiles take
-// smaller stages and more of them.
+// The ring: stages of one k-block, this CTA's rows of A, then of B.  Narrow
+// tiles take smaller stages and more of them.
 constexpr int RING_BYTES = 196608;
 constexpr int MAX_STAGES = 12;
 constexpr int SMEM_BYTES = 1024 + RING_BYTES + EBUFS_BYTES + 1024;
@@ -77,9 +76,8 @@ struct GemmParams {
     int32_t M, N, K;                // GROUP_M: N tokens in all; GROUP_K: K tokens in all
     int32_t tiles_m, tiles_n, total_tiles;  // GROUP_M: tiles_n and total_tiles are found on the device
     int32_t bn;                     // columns of a tile, a multiple of 32 (64 for 16-bit C) up to BN
-    int32_t stages, kps;            // ring: stages, k-blocks in each
-    int32_t a_slot, b_slot;         // bytes of a k-block's parts in the ring
-    int32_t a_load;                 // bytes a copy of A brings
+    int32_t stages;                 // of the ring
+    int32_t a_bytes, b_bytes;       // of a stage
     int32_t band;                   // rows of tiles walked together (GROUP_NONE, GROUP_K)
     int32_t groups, group, offsets64;
     int32_t k_blocks;               // per split (GROUP_NONE)
@@ -379,7 +377,7 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
     // seconds later
     if ((p.group == GROUP_M || (kCe && p.ce.first)) && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
 
-    const int sub_slot = p.a_slot + p.b_slot;
+    const int stage_bytes = p.a_bytes + p.b_bytes;
     const uint32_t ring0 = smem_u32(smem), full0 = smem_u32(full_bar), empty0 = smem_u32(empty_bar);
     const uint32_t full_leader0 = kPair ? mapa_shared(full0, 0) : full0;
     // The i-th tile of this CTA for one of its reading warps; false after the
@@ -436,16 +434,15 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
             const int half = kPair ? tile.n / 2 : tile.n;  // columns this CTA stages
             const int b0 = tile.col0 + rank * half;
             const int a2 = p.group == GROUP_M ? tile.group : 0;
-            const uint32_t tx = static_cast<uint32_t>((kPair ? 2 : 1) * (p.a_load + p.b_slot));
-            for (int kb0 = 0; kb0 < tile.nk; kb0 += p.kps) {
+            const uint32_t tx = static_cast<uint32_t>((kPair ? 2 : 1) * stage_bytes);
+            for (int kb = 0; kb < tile.nk; ++kb) {
                 if (!wait_bounded(empty0 + 8 * stage, phase ^ 1u, abort_flag, p.status)) {
                     ok = false;
                     break;
                 }
                 if (elected) {
                     const uint32_t fl = full_leader0 + 8 * stage;
-                    const int nsub = tile.nk - kb0 < p.kps ? tile.nk - kb0 : p.kps;
-                    if (rank == 0) mbar_expect_tx(full0 + 8 * stage, tx * nsub);
+                    if (rank == 0) mbar_expect_tx(full0 + 8 * stage, tx);
                     auto load3 = [&](uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2) {
                         if (kPair) tma_load_3d_pair(dst, map, c0, c1, c2, fl);
                         else tma_load_3d(dst, map, c0, c1, c2, fl);
@@ -462,15 +459,12 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
                                 load3(dst + static_cast<uint32_t>(c) * MN_CHUNK_BYTES, map, r0 + 64 * c, k, c2);
                         }
                     };
-                    uint32_t sa = ring0 + static_cast<uint32_t>(stage * p.kps * sub_slot);
-                    int k = tile.k0 + kb0 * BK;
-                    for (int q = 0; q < nsub; ++q, sa += sub_slot, k += BK) {
-                        const uint32_t sb = sa + p.a_slot;
-                        if (p.a_mn) load_mn(sa, ma, p.chunked_a, row, BM / 64, k, a2);
-                        else load3(sa, ma, k, row, a2);
-                        if (p.b_mn) load_mn(sb, mb, p.chunked_b, b0, (kPair ? BN / 2 : BN) / 64, k, 0);
-                        else load3(sb, mb, k, b0, 0);
-                    }
+                    const uint32_t sa = ring0 + static_cast<uint32_t>(stage * stage_bytes), sb = sa + p.a_bytes;
+                    const int k = tile.k0 + kb * BK;
+                    if (p.a_mn) load_mn(sa, ma, p.chunked_a, row, BM / 64, k, a2);
+                    else load3(sa, ma, k, row, a2);
+                    if (p.b_mn) load_mn(sb, mb, p.chunked_b, b0, (kPair ? BN / 2 : BN) / 64, k, 0);
+                    else load3(sb, mb, k, b0, 0);
                 }
                 ++issued;
                 if (++stage == p.stages) {
@@ -493,7 +487,7 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
         const bool elected = elect_one();
         // descriptors of the ring's first k-block; others differ in the address
         // field alone (16-byte units, below 2^14 for all of shared memory)
-        const uint64_t desc_a = operand_desc(ring0, 0, p.a_mn), desc_b = operand_desc(ring0 + p.a_slot, 0, p.b_mn);
+        const uint64_t desc_a = operand_desc(ring0, 0, p.a_mn), desc_b = operand_desc(ring0 + p.a_bytes, 0, p.b_mn);
         const uint64_t step_a = p.a_mn ? 16 * 128 / 16 : 32 / 16, step_b = p.b_mn ? 16 * 128 / 16 : 32 / 16;
         for (int i = 0; ok && read_tile(i, tile); ++i) {
             if (tile.nk == 0) continue;
@@ -504,19 +498,15 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
             const uint32_t idesc = p.idesc | (static_cast<uint32_t>(tile.n >> 3) << 17) |
                                    (static_cast<uint32_t>(TILE_M >> 4) << 24);
             const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
-            uint32_t more = 0;  // the tile's first MMA overwrites the accumulator
-            for (int kb0 = 0; ok && kb0 < tile.nk; kb0 += p.kps) {
+            for (int kb = 0; ok && kb < tile.nk; ++kb) {
                 if (!wait_bounded(full0 + 8 * stage, phase, abort_flag, p.status)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const int nsub = tile.nk - kb0 < p.kps ? tile.nk - kb0 : p.kps;
-                uint32_t at = static_cast<uint32_t>(stage * p.kps * sub_slot) >> 4;
-                for (int q = 0; q < nsub; ++q, at += static_cast<uint32_t>(sub_slot) >> 4) {
-                    if (elected) tc_mma_k_block<kPair>(d_tmem, desc_a + at, desc_b + at, idesc, more, step_a, step_b);
-                    more = 1;
-                }
+                const uint64_t at = static_cast<uint32_t>(stage * stage_bytes) >> 4;
+                if (elected)  // the tile's first MMA overwrites the accumulator
+                    tc_mma_k_block<kPair>(d_tmem, desc_a + at, desc_b + at, idesc, kb > 0 ? 1u : 0u, step_a, step_b);
                 if (elected) {
                     if (kPair) tc_commit_pair_mc(empty0 + 8 * stage, 0x3);
                     else tc_commit(empty0 + 8 * stage);
@@ -543,14 +533,12 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
         if (kCe && kPair && p.ce.first && blockIdx.x == 1) write_scalars(p.ce, lane);
     } else {
         // ---------------- epilogue ----------------
-        const int quarter = warp & 3;  // TMEM lanes 32 * quarter .. + 31
-        const int ew = warp - 2;
-        uint8_t* slots = ebufs + NSLOT * ew * EBUF_BYTES;
-        uint32_t seq = 0;  // blocks this warp has written; block n uses slot n % NSLOT and commits one bulk group
+        const int quarter = warp & 3;       // TMEM lanes 32 * quarter .. + 31
+        const int half = (warp - 2) >> 2;   // of the columns
+        uint8_t* buf = ebufs + (warp - 2) * EBUF_BYTES;  // a block on its way to C
         int local = 0;
         const float alpha = p.alpha_dev ? p.alpha * *p.alpha_dev : p.alpha;
-        const int cols = p.c_dtype == MUON_F32 ? 32 : 64;
-        if (kCe && !kPair && p.ce.first && blockIdx.x == 0 && ew == 0) write_scalars(p.ce, lane);
+        if (kCe && !kPair && p.ce.first && blockIdx.x == 0 && warp == 2) write_scalars(p.ce, lane);
         for (int i = 0; read_tile(i, tile); ++i) {
             const int acc = local & 1;
             const uint32_t acc_phase = static_cast<uint32_t>(local >> 1) & 1u;
@@ -562,36 +550,47 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
                 ++local;
             }
             const uint32_t t_addr = tmem_base + static_cast<uint32_t>(acc * BN) + (static_cast<uint32_t>(quarter * 32) << 16);
-            // an empty group adds nothing
-            const bool mine = kEnd != END_TOKENS && row < tile.rows_end && (live || !p.accumulate);
-            const bool by_tma = p.tma_c;
-            if (kEnd == END_TOKENS && row < tile.rows_end) {
+            // this warp has read its last of the accumulator
+            auto release = [&]() {
+                if (!live) return;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (kPair) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty_bar[acc]), 0));
+                    else mbar_arrive(smem_u32(&tempty_bar[acc]));
+                }
+            };
+            // the block buffer is free again once its last tensor store has read it
+            auto claim = [&]() {
+                if (lane == 0) bulk_wait_read<0>();
+                __syncwarp();
+            };
+            const int sw = lane & 7;  // swizzle of this lane's row: 16-byte chunk q sits at q ^ sw
+            if (kEnd == END_TOKENS) {
                 // 32 tokens at a time, transposed through shared memory: the
                 // lanes (features) write side by side into each token's 64
                 // bytes, and a tensor store takes the block to C.  A group's
                 // last tokens are stored one by one.
                 const int cols = tile.cols_end - tile.col0;
-                uint16_t* out = static_cast<uint16_t*>(p.C) + row + lane;
-                for (int c = 0; c < cols; c += 32) {
+                const bool mine = row < tile.rows_end;
+                for (int c = 32 * half; mine && c < cols; c += 64) {
                     float v[32];
                     if (live) {
                         tmem_load_32cols(t_addr + static_cast<uint32_t>(c), v);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = 0.f;
+                        for (int k = 0; k < 32; ++k) v[k] = 0.f;
                     }
                     uint32_t w[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) w[i] = pack16(v[2 * i], v[2 * i + 1], p.c_dtype);
-                    if (by_tma && c + 32 <= cols) {
-                        uint8_t* buf = slots + (seq % NSLOT) * EBUF_BYTES;
-                        if (lane == 0) bulk_wait_read<NSLOT - 1>();
-                        __syncwarp();
+                    for (int k = 0; k < 16; ++k) w[k] = pack16(v[2 * k], v[2 * k + 1], p.c_dtype);
+                    if (p.tma_c && c + 32 <= cols) {
+                        claim();
                         uint16_t* b = reinterpret_cast<uint16_t*>(buf) + lane;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            b[64 * i] = static_cast<uint16_t>(w[i]);
-                            b[64 * i + 32] = static_cast<uint16_t>(w[i] >> 16);
+                        for (int k = 0; k < 16; ++k) {
+                            b[64 * k] = static_cast<uint16_t>(w[k]);
+                            b[64 * k + 32] = static_cast<uint16_t>(w[k] >> 16);
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
@@ -599,108 +598,113 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
                             tma_store_3d(&p.tm_c, smem_u32(buf), row, tile.col0 + c, 0);
                             bulk_commit();
                         }
-                        ++seq;
                     } else if (row + lane < tile.rows_end) {
-                        uint16_t* o = out + static_cast<int64_t>(tile.col0 + c) * p.ldc;
+                        uint16_t* o = static_cast<uint16_t*>(p.C) + static_cast<int64_t>(tile.col0 + c) * p.ldc + row + lane;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i, o += p.ldc)
-                            if (c + i < cols) *o = static_cast<uint16_t>(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
+                        for (int k = 0; k < 32; ++k, o += p.ldc)
+                            if (c + k < cols) *o = static_cast<uint16_t>(k & 1 ? w[k / 2] >> 16 : w[k / 2]);
                     }
                 }
-            }
-            RowSums rs = {-INFINITY, 0.f};
-            int target = -1;
-            if (kCe && mine && row + lane < p.M) {
-                const int64_t tg = load_index(p.ce.targets, p.ce.targets64, row + lane);
-                target = tg >= 0 && tg < p.N ? static_cast<int>(tg) : -1;
-            }
-            if (mine) {
-                for (int c = 0; c < p.bn; c += cols) {
+                release();
+            } else if (kCe) {
+                // the tile's halves of the columns, in steps of 32
+                const int mid = (p.bn / 2 + 31) & ~31, lo = half ? mid : 0, hi = half ? p.bn : mid;
+                const bool mine = row < tile.rows_end;
+                RowSums rs = {-INFINITY, 0.f};
+                int target = -1;
+                if (mine && row + lane < p.M) {
+                    const int64_t tg = load_index(p.ce.targets, p.ce.targets64, row + lane);
+                    target = tg >= 0 && tg < p.N ? static_cast<int>(tg) : -1;
+                }
+                for (int c = lo; mine && c < hi && tile.col0 + c < p.N; c += 32) {
                     const int col = tile.col0 + c;
-                    if (col >= p.N) break;
-                    const uint32_t b = seq % NSLOT;
-                    uint8_t* buf = slots + b * EBUF_BYTES;
-                    const bool out = !kCe || p.ce.store;
-                    if (out) {
-                        if (lane == 0) bulk_wait_read<NSLOT - 1>();
+                    float v[32];
+                    tmem_load_32cols(t_addr + static_cast<uint32_t>(c), v);
+                    if (p.ce.store) {
+                        claim();
+                        uint8_t* brow = buf + lane * 128;
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            *reinterpret_cast<float4*>(brow + ((q ^ sw) << 4)) =
+                                make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                        fence_proxy_async_smem();
                         __syncwarp();
+                        if (lane == 0) {
+                            tma_store_3d(&p.tm_c, smem_u32(buf), col, row, 0);
+                            bulk_commit();
+                        }
                     }
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) v[k] *= p.ce.scale2;
+                    const int off = target - col;
+                    if (__any_sync(0xffffffffu, off >= 0 && off < 32)) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (k == off) v[k] = -INFINITY;
+                    }
+                    if (col + 32 > p.N) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (col + k >= p.N) v[k] = -INFINITY;
+                    }
+                    rs.add(v);
+                }
+                release();
+                if (mine && row + lane < p.M)
+                    p.ce.sums[(static_cast<int64_t>(row + lane) * p.tiles_n + tile.tn) * 2 + half] = make_float2(rs.top, rs.sum);
+            } else {
+                // the tile's halves of 128 columns, in blocks of 128 bytes a
+                // row; an empty group adds nothing
+                const int cols = p.c_dtype == MUON_F32 ? 32 : 64;
+                const bool mine = row < tile.rows_end && (live || !p.accumulate);
+                for (int c = half * (BN / 2); mine && c < (half + 1) * (BN / 2) && tile.col0 + c < p.N; c += cols) {
+                    const int col = tile.col0 + c;
                     uint8_t* brow = buf + lane * 128;
-                    const int sw = lane & 7;
-                    for (int h = 0; h < cols; h += 32) {
+                    if (cols == 32) {
                         float v[32];
                         if (live) {
-                            tmem_load_32cols(t_addr + static_cast<uint32_t>(c + h), v);
+                            tmem_load_32cols(t_addr + static_cast<uint32_t>(c), v);
                         } else {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] = 0.f;
+                            for (int k = 0; k < 32; ++k) v[k] = 0.f;
                         }
-                        if (kCe) {
-                            if (out) {
+                        claim();
 #pragma unroll
-                                for (int q = 0; q < 8; ++q)
-                                    *reinterpret_cast<float4*>(brow + ((q ^ sw) << 4)) =
-                                        make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-                            }
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] *= p.ce.scale2;
-                            const int off = target - col;
-                            if (__any_sync(0xffffffffu, off >= 0 && off < 32)) {
-#pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    if (i == off) v[i] = -INFINITY;
-                            }
-                            if (col + 32 > p.N) {
-#pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    if (col + i >= p.N) v[i] = -INFINITY;
-                            }
-                            rs.add(v);
+                        for (int q = 0; q < 8; ++q)
+                            *reinterpret_cast<float4*>(brow + ((q ^ sw) << 4)) = make_float4(
+                                alpha * v[4 * q], alpha * v[4 * q + 1], alpha * v[4 * q + 2], alpha * v[4 * q + 3]);
+                    } else {
+                        float v[64];
+                        if (live) {
+                            tmem_load_64cols(t_addr + static_cast<uint32_t>(c), v);
                         } else {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] *= alpha;
-                            if (cols == 32) {
-#pragma unroll
-                                for (int q = 0; q < 8; ++q)
-                                    *reinterpret_cast<float4*>(brow + ((q ^ sw) << 4)) =
-                                        make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-                            } else {
-#pragma unroll
-                                for (int q = 0; q < 4; ++q)
-                                    *reinterpret_cast<uint4*>(brow + (((h / 8 + q) ^ sw) << 4)) =
-                                        make_uint4(pack16(v[8 * q], v[8 * q + 1], p.c_dtype),
-                                                   pack16(v[8 * q + 2], v[8 * q + 3], p.c_dtype),
-                                                   pack16(v[8 * q + 4], v[8 * q + 5], p.c_dtype),
-                                                   pack16(v[8 * q + 6], v[8 * q + 7], p.c_dtype));
-                            }
+                            for (int k = 0; k < 64; ++k) v[k] = 0.f;
                         }
+                        uint32_t w[32];
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) w[k] = pack16(alpha * v[2 * k], alpha * v[2 * k + 1], p.c_dtype);
+                        claim();
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            *reinterpret_cast<uint4*>(brow + ((q ^ sw) << 4)) =
+                                make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
                     }
-                    if (!out) continue;
-                    if (by_tma) {
+                    if (p.tma_c) {
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
                             if (p.accumulate) tma_add_3d(&p.tm_c, smem_u32(buf), col, row, tile.c2);
                             else tma_store_3d(&p.tm_c, smem_u32(buf), col, row, tile.c2);
+                            bulk_commit();
                         }
                     } else {
                         __syncwarp();
                         store_rows(p, buf, row, tile.rows_end, col, tile.c2, lane);
                         __syncwarp();
                     }
-                    if (lane == 0) bulk_commit();
-                    ++seq;
                 }
-            }
-            if (kCe && mine && row + lane < p.M)
-                p.ce.sums[static_cast<int64_t>(row + lane) * p.tiles_n + tile.tn] = make_float2(rs.top, rs.sum);
-            if (live) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (kPair) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty_bar[acc]), 0));
-                    else mbar_arrive(smem_u32(&tempty_bar[acc]));
-                }
+                release();
             }
         }
         // the output stores complete before the CTA exits
@@ -923,12 +927,12 @@ int64_t train_gemm_bn(int64_t M, int64_t N) {
     return best;
 }
 
-int64_t train_gemm_col_tiles(int64_t M, int64_t N) {
+int64_t train_gemm_sums(int64_t M, int64_t N) {
     const int64_t bn = train_gemm_bn(M, N);
-    return (N + bn - 1) / bn;
+    return 2 * ((N + bn - 1) / bn);
 }
 
-int64_t train_gemm_max_col_tiles(int64_t N) { return (N + 127) / 128; }
+int64_t train_gemm_max_sums(int64_t N) { return 2 * ((N + 127) / 128); }
 
 cudaError_t train_gemm(const TrainGemm& g, int num_sms, cudaStream_t st) {
     int max_pairs = 0;
@@ -951,10 +955,9 @@ cudaError_t train_gemm(const TrainGemm& g, int num_sms, cudaStream_t st) {
     // A's rows past a short product's are neither loaded nor stored: the MMA
     // reads what the ring holds there
     const int32_t a_rows = !g.a_mn && g.group == GROUP_NONE && g.M < BM ? static_cast<int32_t>(round_up(g.M, 8)) : BM;
-    p.a_slot = p.a_load = a_rows * BK * 2;
-    p.b_slot = static_cast<int32_t>(pair ? bn / 2 : bn) * BK * 2;
-    p.kps = pair ? 2 : 1;
-    p.stages = RING_BYTES / (p.kps * (p.a_slot + p.b_slot));
+    p.a_bytes = a_rows * BK * 2;
+    p.b_bytes = static_cast<int32_t>(pair ? bn / 2 : bn) * BK * 2;
+    p.stages = RING_BYTES / (p.a_bytes + p.b_bytes);
     if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
     bool ok = true;
     // the widths of MN-major operands are rounded up where the row pitch
