@@ -67,6 +67,7 @@ enum { END_STORE = 0, END_CE = 1, END_TOKENS = 2 };
 struct GemmParams {
     CUtensorMap tm_a, tm_b, tm_c;
     const CUtensorMap* group_maps;  // GROUP_K: A's and B's map of each group
+    const int32_t* order;           // GROUP_K: the groups, largest first
     const void* offsets;
     void* C;
     const float* alpha_dev;
@@ -131,8 +132,9 @@ struct Walker {
         if (p.group != GROUP_M) {
             if (t >= p.total_tiles) return false;
             const int per = p.tiles_m * p.tiles_n;
-            const int s = t / per;
+            int s = t / per;
             const int r = t - s * per;
+            if (p.group == GROUP_K) s = p.order[s];
             const int span = p.band * p.tiles_n;
             const int b = r / span;
             const int rr = r - b * span;
@@ -228,13 +230,22 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-__device__ __forceinline__ uint32_t pack16(float lo, float hi, int dtype) {
+// 2 N fp32 values rounded to 16 bits, in pairs.
+template <int N>
+__device__ __forceinline__ void pack_row(const float (&v)[2 * N], uint32_t (&w)[N], int dtype) {
     if (dtype == MUON_BF16) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t*>(&v);
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const __nv_bfloat162 x = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+            w[k] = *reinterpret_cast<const uint32_t*>(&x);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const __half2 x = __floats2half2_rn(v[2 * k], v[2 * k + 1]);
+            w[k] = *reinterpret_cast<const uint32_t*>(&x);
+        }
     }
-    const __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // The finished block in shared memory (32 rows of 128 bytes, swizzled) to a C
@@ -396,8 +407,12 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
         // ---------------- tiles ----------------
         Walker<TILE_M> walk(p, lane);
         int i = 0;
-        for (int t = worker;; t += workers, ++i) {
-            const bool more = walk.next(t, tile);
+        for (;; ++i) {
+            // groups of falling size are dealt out to and fro: the workers' sums
+            // of k-blocks end within 2% of each other where one direction leaves
+            // 4%, and groups in their given order 8 to 16%
+            const bool back = p.group == GROUP_K && (i & 1);
+            const bool more = walk.next(i * workers + (back ? workers - 1 - worker : worker), tile);
             const int s = i % TILE_SLOTS;
             if (!wait_bounded(smem_u32(&sempty_bar[s]), (static_cast<uint32_t>(i / TILE_SLOTS) & 1u) ^ 1u, abort_flag,
                               p.status))
@@ -434,6 +449,9 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
             const int half = kPair ? tile.n / 2 : tile.n;  // columns this CTA stages
             const int b0 = tile.col0 + rank * half;
             const int a2 = p.group == GROUP_M ? tile.group : 0;
+            // a tile narrower than the stage still takes its rows in one copy: a
+            // copy costs more than the neighbours' rows that it brings (boxes of
+            // 32 rows: the experts' products 6% slower)
             const uint32_t tx = static_cast<uint32_t>((kPair ? 2 : 1) * stage_bytes);
             for (int kb = 0; kb < tile.nk; ++kb) {
                 if (!wait_bounded(empty0 + 8 * stage, phase ^ 1u, abort_flag, p.status)) {
@@ -550,14 +568,16 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
                 ++local;
             }
             const uint32_t t_addr = tmem_base + static_cast<uint32_t>(acc * BN) + (static_cast<uint32_t>(quarter * 32) << 16);
-            // this warp has read its last of the accumulator
+            // this warp has read its last of the accumulator: handed back before
+            // the last block is stored, and without waiting for stores
+            // (2048-row experts of 512 tokens: a release after them took 3400 of
+            // 6900 cycles a tile)
             auto release = [&]() {
                 if (!live) return;
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    if (kPair) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty_bar[acc]), 0));
-                    else mbar_arrive(smem_u32(&tempty_bar[acc]));
+                    mbar_arrive_cluster_relaxed(kPair ? mapa_shared(smem_u32(&tempty_bar[acc]), 0) : smem_u32(&tempty_bar[acc]));
                 }
             };
             // the block buffer is free again once its last tensor store has read it
@@ -572,7 +592,8 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
                 // bytes, and a tensor store takes the block to C.  A group's
                 // last tokens are stored one by one.
                 const int cols = tile.cols_end - tile.col0;
-                const bool mine = row < tile.rows_end;
+                const bool mine = row < tile.rows_end && 32 * half < cols;
+                if (!mine) release();
                 for (int c = 32 * half; mine && c < cols; c += 64) {
                     float v[32];
                     if (live) {
@@ -581,9 +602,9 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
 #pragma unroll
                         for (int k = 0; k < 32; ++k) v[k] = 0.f;
                     }
+                    if (c + 64 >= cols) release();
                     uint32_t w[16];
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) w[k] = pack16(v[2 * k], v[2 * k + 1], p.c_dtype);
+                    pack_row<16>(v, w, p.c_dtype);
                     if (p.tma_c && c + 32 <= cols) {
                         claim();
                         uint16_t* b = reinterpret_cast<uint16_t*>(buf) + lane;
@@ -605,11 +626,11 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
                             if (c + k < cols) *o = static_cast<uint16_t>(k & 1 ? w[k / 2] >> 16 : w[k / 2]);
                     }
                 }
-                release();
             } else if (kCe) {
                 // the tile's halves of the columns, in steps of 32
                 const int mid = (p.bn / 2 + 31) & ~31, lo = half ? mid : 0, hi = half ? p.bn : mid;
-                const bool mine = row < tile.rows_end;
+                const bool mine = row < tile.rows_end && tile.col0 + lo < p.N;
+                if (!mine) release();
                 RowSums rs = {-INFINITY, 0.f};
                 int target = -1;
                 if (mine && row + lane < p.M) {
@@ -620,6 +641,7 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
                     const int col = tile.col0 + c;
                     float v[32];
                     tmem_load_32cols(t_addr + static_cast<uint32_t>(c), v);
+                    if (c + 32 >= hi || col + 32 >= p.N) release();
                     if (p.ce.store) {
                         claim();
                         uint8_t* brow = buf + lane * 128;
@@ -649,15 +671,16 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
                     }
                     rs.add(v);
                 }
-                release();
-                if (mine && row + lane < p.M)
+                if (row < tile.rows_end && row + lane < p.M)
                     p.ce.sums[(static_cast<int64_t>(row + lane) * p.tiles_n + tile.tn) * 2 + half] = make_float2(rs.top, rs.sum);
             } else {
                 // the tile's halves of 128 columns, in blocks of 128 bytes a
                 // row; an empty group adds nothing
                 const int cols = p.c_dtype == MUON_F32 ? 32 : 64;
-                const bool mine = row < tile.rows_end && (live || !p.accumulate);
-                for (int c = half * (BN / 2); mine && c < (half + 1) * (BN / 2) && tile.col0 + c < p.N; c += cols) {
+                const int lo = half * (BN / 2), hi = min(lo + BN / 2, p.N - tile.col0);
+                const bool mine = row < tile.rows_end && lo < hi && (live || !p.accumulate);
+                if (!mine) release();
+                for (int c = lo; mine && c < hi; c += cols) {
                     const int col = tile.col0 + c;
                     uint8_t* brow = buf + lane * 128;
                     if (cols == 32) {
@@ -668,6 +691,7 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
 #pragma unroll
                             for (int k = 0; k < 32; ++k) v[k] = 0.f;
                         }
+                        if (c + cols >= hi) release();
                         claim();
 #pragma unroll
                         for (int q = 0; q < 8; ++q)
@@ -681,9 +705,13 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
 #pragma unroll
                             for (int k = 0; k < 64; ++k) v[k] = 0.f;
                         }
-                        uint32_t w[32];
+                        if (c + cols >= hi) release();
+                        if (alpha != 1.f) {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) w[k] = pack16(alpha * v[2 * k], alpha * v[2 * k + 1], p.c_dtype);
+                            for (int k = 0; k < 64; ++k) v[k] *= alpha;
+                        }
+                        uint32_t w[32];
+                        pack_row<32>(v, w, p.c_dtype);
                         claim();
 #pragma unroll
                         for (int q = 0; q < 8; ++q)
@@ -704,7 +732,6 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
                         __syncwarp();
                     }
                 }
-                release();
             }
         }
         // the output stores complete before the CTA exits
@@ -736,22 +763,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 }
 
 // GROUP_K: a copy of A's and B's tensor map for every group, its row extent
-// cut at the group's end.  Also clears the status word.
+// cut at the group's end; by the last CTA, the groups in the order of falling
+// size (given order for equal ones, and beyond 1024 groups).  Also clears the
+// status word.
 struct GroupMapParams {
     CUtensorMap a, b;
     CUtensorMap* out;
+    int32_t* order;
     const void* offsets;
     int* status;
     int32_t groups, offsets64, rows;
 };
 
-__global__ void group_maps_kernel(const __grid_constant__ GroupMapParams p) {
+constexpr int kMapThreads = 128;
+constexpr int kMaxOrdered = 1024;
+
+__global__ void __launch_bounds__(kMapThreads) group_maps_kernel(const __grid_constant__ GroupMapParams p) {
+    __shared__ int size[kMaxOrdered];
     pdl_wait_then_release();
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
-    const int i = blockIdx.x * blockDim.x + threadIdx.x;
+    auto edge = [&](int e) {
+        const int64_t o = load_index(p.offsets, p.offsets64, e);
+        return o < 0 ? 0 : o > p.rows ? p.rows : static_cast<int>(o);
+    };
+    if (blockIdx.x + 1 == gridDim.x) {
+        if (threadIdx.x == 0) *p.status = 0;
+        const bool sort = p.groups <= kMaxOrdered;
+        for (int e = threadIdx.x; e < p.groups; e += kMapThreads) {
+            if (sort) size[e] = max(edge(e + 1) - edge(e), 0);
+            else p.order[e] = e;
+        }
+        if (!sort) return;
+        __syncthreads();
+        for (int e = threadIdx.x; e < p.groups; e += kMapThreads) {
+            int rank = 0;
+            for (int f = 0; f < p.groups; ++f) rank += size[f] > size[e] || (size[f] == size[e] && f < e);
+            p.order[rank] = e;
+        }
+        return;
+    }
+    const int i = blockIdx.x * kMapThreads + threadIdx.x;
     if (i >= 2 * p.groups) return;
-    const int64_t o = load_index(p.offsets, p.offsets64, (i >> 1) + 1);
-    const uint32_t end = o < 1 ? 1u : o > p.rows ? static_cast<uint32_t>(p.rows) : static_cast<uint32_t>(o);
+    const uint32_t end = static_cast<uint32_t>(max(edge((i >> 1) + 1), 1));
     const uint4* src = reinterpret_cast<const uint4*>(i & 1 ? &p.b : &p.a);
     uint4* dst = reinterpret_cast<uint4*>(p.out + i);
 #pragma unroll
@@ -905,7 +957,7 @@ int64_t train_gemm_tiles(int64_t M, int64_t N) {
     return ((M + tm - 1) / tm) * ((N + BN - 1) / BN);
 }
 
-size_t train_gemm_group_bytes(int64_t groups) { return static_cast<size_t>(groups) * 2 * sizeof(CUtensorMap); }
+size_t train_gemm_group_bytes(int64_t groups) { return static_cast<size_t>(groups) * (2 * sizeof(CUtensorMap) + 4); }
 
 // Columns of a plain product's tiles when B is K-major: the width whose tiles
 // fill the last wave of CTAs best.  16 rows against 163840 columns: 224
@@ -1025,14 +1077,16 @@ cudaError_t train_gemm(const TrainGemm& g, int num_sms, cudaStream_t st) {
         m.a = p.tm_a;
         m.b = p.tm_b;
         m.out = static_cast<CUtensorMap*>(g.group_maps);
+        m.order = reinterpret_cast<int32_t*>(m.out + 2 * g.groups);
         m.offsets = g.offsets;
         m.status = g.status;
         m.groups = p.groups;
         m.offsets64 = g.offsets64;
         m.rows = p.K;
         p.group_maps = m.out;
+        p.order = m.order;
         launch_begin(g.kind, st);
-        e = launch_pdl(group_maps_kernel, dim3((2 * p.groups + 63) / 64), dim3(64), 0, st, m);
+        e = launch_pdl(group_maps_kernel, dim3((2 * p.groups + kMapThreads - 1) / kMapThreads + 1), dim3(kMapThreads), 0, st, m);
         launch_end(g.kind, st);
         if (e != cudaSuccess) return e;
     }
