@@ -14,8 +14,8 @@
 //   sort   the first CTA sorts, least significant digit first, ids in
 //          registers; the others meanwhile write the zero rows, each for its
 //          share of the table, after a look through all ids
-//   sums   per 32 sorted positions and 256 columns, the sums of the runs of
-//          equal ids: a run inside its 32 goes straight to its row, the
+//   sums   per 8 to 32 sorted positions and 256 columns, the sums of the runs of
+//          equal ids: a run inside them goes straight to its row, the
 //          pieces of one that crosses go to the workspace
 //   join   the crossing runs' pieces, in order
 // More tokens are sorted by several CTAs, three launches a digit, and the
@@ -421,7 +421,8 @@ __global__ void __launch_bounds__(1024) sort_scan_kernel(uint32_t* hist, int64_t
 // ---------------------------------------------------------------------------
 // Sums
 // ---------------------------------------------------------------------------
-constexpr int kPiece = 32;     // sorted positions of one warp's task
+constexpr int kMaxPiece = 32;  // sorted positions of one warp's task: 8, 16 or 32, see launch_embed_grad
+constexpr int kMinPiece = 8;
 constexpr int kCols = 256;     // and columns: 8 per lane
 constexpr int kSumWarps = 4;
 constexpr int kZeroRows = 32;  // table rows of one warp's zero task
@@ -434,7 +435,7 @@ struct SumArgs {
     float* parts;          // [2 * piece + slot][part_ld]: slot 0 a run that began before, 1 one that goes on
     float* d_table;
     int64_t grad_ld, part_ld, vocab, dim;
-    int32_t tokens, pieces, col_tasks, zero_tasks_x, accumulate;
+    int32_t tokens, piece, pieces, col_tasks, zero_tasks_x, accumulate;
     int32_t sum_blocks;    // blocks before the zero tasks' ones
     float scale;
 };
@@ -474,8 +475,8 @@ template <int GD, bool kWide>
 __device__ __forceinline__ void sum_piece(const SumArgs& a, int piece, int64_t c0, int lane) {
     typedef typename Elem<GD>::T TG;
     const TG* grad = static_cast<const TG*>(a.grad);
-    const int i0 = piece * kPiece;
-    const int n = a.tokens - i0 < kPiece ? a.tokens - i0 : kPiece;
+    const int i0 = piece * a.piece;
+    const int n = a.tokens - i0 < a.piece ? a.tokens - i0 : a.piece;
     const int dead = static_cast<int>(a.vocab);
     const int key = lane < n ? a.keys[i0 + lane] : dead;
     const int pos = lane < n ? a.pos[i0 + lane] : 0;
@@ -486,7 +487,7 @@ __device__ __forceinline__ void sum_piece(const SumArgs& a, int piece, int64_t c
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.f;
     bool began = __shfl_sync(0xffffffffu, key, 0) != prev;  // the current run's first token is in this piece
-    constexpr int kBatch = kWide && GD != MUON_F32 ? 8 : 4;  // tokens loaded together: 32 registers
+    constexpr int kBatch = kWide && GD == MUON_F32 ? 4 : 8;  // tokens loaded together
     for (int j0 = 0; j0 < live; j0 += kBatch) {
         typename std::conditional<kWide, Raw8<GD>, float[8]>::type v[kBatch];
 #pragma unroll
@@ -573,7 +574,7 @@ __device__ __forceinline__ void zero_rows(const SumArgs& a, int64_t v0, int64_t 
 }
 
 template <int GD, bool kWide>
-__global__ void __launch_bounds__(32 * kSumWarps, 6) embed_sum_kernel(const __grid_constant__ SumArgs a) {
+__global__ void __launch_bounds__(32 * kSumWarps, kWide ? 6 : 4) embed_sum_kernel(const __grid_constant__ SumArgs a) {
     pdl_wait_then_release();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (static_cast<int>(blockIdx.x) < a.sum_blocks) {
@@ -612,14 +613,14 @@ __global__ void __launch_bounds__(256) embed_join_kernel(const __grid_constant__
     pdl_wait_then_release();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int piece = blockIdx.x;
-    const int start = piece * kPiece, end = start + kPiece;
+    const int start = piece * a.piece, end = start + a.piece;
     if (end >= a.tokens) return;
     const int key = a.keys[end - 1], after = a.keys[end], head = a.keys[start], before = start > 0 ? a.keys[start - 1] : -1;
     // no run crosses, or the one that does began before this piece
     if (key == static_cast<int>(a.vocab) || after != key || (head == key && before == key)) return;
     int count = 1;  // pieces of the run: those whose first key is its key
     for (;;) {
-        const int64_t first = (piece + count + lane) * static_cast<int64_t>(kPiece);
+        const int64_t first = (piece + count + lane) * static_cast<int64_t>(a.piece);
         const int n = __popc(__ballot_sync(0xffffffffu, first < a.tokens && a.keys[first < a.tokens ? first : 0] == key));
         count += n;
         if (n < 32) break;
@@ -660,6 +661,16 @@ struct GradLayout {
     size_t keys, pos, keys2, pos2, hist, parts, total;
 };
 
+// Long pieces leave fewer runs to join, short ones more warps: the longest
+// that gives every warp slot of 152 SMs (24 each) a task, as 32 does for 16384
+// tokens of 7168 (4099 tokens of 1003: 64 us with 32, PIECEUS with 8).
+int sum_piece_size(int64_t tokens, int64_t dim) {
+    const int64_t cols = (dim + kCols - 1) / kCols;
+    int piece = kMaxPiece;
+    while (piece > kMinPiece && (tokens + piece - 1) / piece * cols < 152 * 24) piece /= 2;
+    return piece;
+}
+
 GradLayout grad_layout(int64_t tokens, int64_t dim) {
     GradLayout L = {};
     auto take = [&L](int64_t bytes) {
@@ -675,7 +686,8 @@ GradLayout grad_layout(int64_t tokens, int64_t dim) {
     L.keys2 = take(L.tiles > 1 ? 4 * tokens : 0);
     L.pos2 = take(L.tiles > 1 ? 4 * tokens : 0);
     L.hist = take(L.tiles > 1 ? 4 * L.tiles * kBins : 0);
-    L.parts = take(8 * ((tokens + kPiece - 1) / kPiece) * L.part_ld);
+    const int64_t piece = sum_piece_size(tokens, dim);
+    L.parts = take(8 * ((tokens + piece - 1) / piece) * L.part_ld);
     return L;
 }
 
@@ -792,8 +804,9 @@ cudaError_t launch_embed_grad(const EmbedGrad& a, void* workspace, int num_sms, 
     m.vocab = a.vocab;
     m.dim = a.dim;
     m.tokens = static_cast<int32_t>(a.tokens);
-    m.pieces = static_cast<int32_t>((a.tokens + kPiece - 1) / kPiece);
     m.col_tasks = static_cast<int32_t>((a.dim + kCols - 1) / kCols);
+    m.piece = sum_piece_size(a.tokens, a.dim);
+    m.pieces = static_cast<int32_t>((a.tokens + m.piece - 1) / m.piece);
     m.zero_tasks_x = static_cast<int32_t>((a.dim + kZeroCols - 1) / kZeroCols);
     m.accumulate = a.accumulate;
     m.scale = a.scale;
