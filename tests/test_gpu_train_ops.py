@@ -661,3 +661,57 @@ def test_host_buffers_are_refused(lib):
     assert lib.muon_expert_matmul(x.data_ptr(), 16, w.data_ptr(), off.data_ptr(), 0, 1, 1, 5, 16, 16, 0, y.data_ptr(), 16,
                                   ws.data_ptr(), ws.numel(), st) == 1
     assert (y == 1).all()
+
+
+# --------------------------------------------------------------------------
+# Offsets past 32 bits
+# --------------------------------------------------------------------------
+
+def test_expert_weights_past_32_bit_offsets(lib):
+    """600 experts of 2048 x 2048 (2.5e9 weights); tokens at both ends."""
+    e, d = 600, 2048
+    w = torch.zeros(e, d, d, dtype=BF, device=DEV)
+    g = gen(111)
+    w[0], w[-1] = randn(g, (d, d), 0.05, BF), randn(g, (d, d), 0.05, BF)
+    x = randn(g, (40, d), 1.0, BF)
+    off = torch.full((e + 1,), 25, dtype=torch.int32, device=DEV)
+    off[0], off[-1] = 0, 40
+    for tr in (False, True):
+        y = m.muon_expert_matmul(x, w, off, transpose=tr)
+        for s, i in ((slice(0, 25), 0), (slice(25, 40), e - 1)):
+            wd = w[i].double() if tr else w[i].double().t()
+            want = x[s].double() @ wd
+            within(y[s], want, rounded(mma_bound(d, x[s].double().abs() @ wd.abs()), want, BF), "y")
+    dw = m.muon_expert_wgrad(y, x, off, out=w)
+    for s, i in ((slice(0, 25), 0), (slice(25, 40), e - 1)):
+        want = y[s].double().t() @ x[s].double()
+        within(dw[i], want, rounded(mma_bound(25, y[s].double().abs().t() @ x[s].double().abs()), want, BF), "dw")
+    assert (dw[1:-1].view(torch.int64) == 0).all()
+
+
+def test_head_past_32_bit_offsets(lib):
+    """300000 x 8192 head weights (2.5e9), targets in its first and last rows."""
+    v, d = 300000, 8192
+    g = gen(112)
+    w = torch.empty(v, d, dtype=BF, device=DEV).normal_(0, 0.01, generator=g)
+    h = randn(g, (5, d), 1.0, BF)
+    t = torch.tensor([v - 1, 0, 299000, 5, v - 1], device=DEV)
+    loss, lse, dh, dw = m.muon_linear_ce_grad(h, w, t)
+    z = torch.cat([h.double() @ part.double().t() for part in w.split(20000)], dim=1)
+    want = torch.logsumexp(z, 1)
+    dz = mma_bound(d, (h.double().abs() @ w[:2000].double().abs().t()).max().item())  # random rows are alike
+    assert ((lse.double() - want).abs() <= 2 * dz + 1e-5).all()
+    p = torch.exp(z - want[:, None])
+    p[torch.arange(5), t] -= 1
+    tail = p[:, -1000:].t() @ h.double()
+    mag = p[:, -1000:].abs().t() @ h.double().abs()
+    within(dw[-1000:], tail, (2.0 ** -8 + 2 * dz) * mag + 2.0 ** -8 * tail.abs() + mma_bound(5, mag), "last rows of d_weight")
+
+
+def test_embedding_grad_past_32_bit_offsets(lib):
+    v, d = 300000, 8192
+    grad = torch.ones(3, d, dtype=BF, device=DEV)
+    ids = torch.tensor([v - 1, 7, v - 1], device=DEV)
+    out = m.muon_embedding_grad(grad, ids, v)
+    assert (out[v - 1] == 2).all() and (out[7] == 1).all() and (out[v - 2] == 0).all()
+    assert out.sum(dtype=torch.float64).item() == 3 * d
