@@ -64,11 +64,8 @@ constexpr int SMEM_BYTES = 1024 + RING_BYTES + EBUFS_BYTES + 1024;
 // What a product's tiles end in.
 enum { END_STORE = 0, END_CE = 1, END_TOKENS = 2 };
 
-constexpr int TOKEN_BOXES = 8;
-
 struct GemmParams {
     CUtensorMap tm_a, tm_b, tm_c;
-    CUtensorMap tm_tokens[TOKEN_BOXES];  // GROUP_M: B in boxes of 1 .. 8 eighths of a stage's rows
     const CUtensorMap* group_maps;  // GROUP_K: A's and B's map of each group
     const int32_t* order;           // GROUP_K: the groups, largest first
     const void* offsets;
@@ -452,17 +449,10 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
             const int half = kPair ? tile.n / 2 : tile.n;  // columns this CTA stages
             const int b0 = tile.col0 + rank * half;
             const int a2 = p.group == GROUP_M ? tile.group : 0;
-            int b_bytes = p.b_bytes;
-            if (kEnd == END_TOKENS) {
-                // the tile's rows in one copy of the smallest box that holds them:
-                // copies feed an SM 64 bytes a cycle, what a full k-block's MMAs
-                // take, and several small ones less (boxes of 32 rows: 6% slower)
-                const int unit = b_bytes / (BK * 2 * TOKEN_BOXES);
-                const int eighths = (half + unit - 1) / unit;
-                mb = &p.tm_tokens[eighths - 1];
-                b_bytes = eighths * unit * BK * 2;
-            }
-            const uint32_t tx = static_cast<uint32_t>((kPair ? 2 : 1) * (p.a_bytes + b_bytes));
+            // a tile narrower than the stage still takes its rows in one copy: a
+            // copy costs more than the neighbours' rows that it brings (boxes of
+            // 32 rows: the experts' products 6% slower)
+            const uint32_t tx = static_cast<uint32_t>((kPair ? 2 : 1) * stage_bytes);
             for (int kb = 0; kb < tile.nk; ++kb) {
                 if (!wait_bounded(empty0 + 8 * stage, phase ^ 1u, abort_flag, p.status)) {
                     ok = false;
@@ -1011,7 +1001,7 @@ cudaError_t train_gemm(const TrainGemm& g, int num_sms, cudaStream_t st) {
     } else if (end == END_TOKENS) {
         // about the tokens of two average experts, so that few experts need two tiles
         const int64_t want = 2 * ((g.N + g.groups - 1) / g.groups);
-        bn = pair || want > 128 ? 256 : want > 64 ? 128 : 64;
+        bn = pair || want > 128 ? 256 : want > 64 ? 128 : want > 32 ? 64 : 32;
     }
     p.bn = static_cast<int32_t>(bn);
     // A's rows past a short product's are neither loaded nor stored: the MMA
@@ -1032,10 +1022,7 @@ cudaError_t train_gemm(const TrainGemm& g, int num_sms, cudaStream_t st) {
     if (!g.a_mn) ok &= map3(&p.tm_a, g.A, g.dtype, g.K, g.M, a_count, g.lda, g.a_stride, static_cast<uint32_t>(a_rows));
     else if (p.chunked_a) ok &= map_chunked(&p.tm_a, g.A, g.dtype, wa, g.K, a_count, g.lda, g.a_stride);
     else ok &= map3(&p.tm_a, g.A, g.dtype, g.M, g.K, a_count, g.lda, g.a_stride, BK);
-    const int64_t b_rows = pair ? bn / 2 : bn;
-    for (int i = 0; i < TOKEN_BOXES && end == END_TOKENS; ++i)
-        ok &= map3(&p.tm_tokens[i], g.B, g.dtype, g.K, g.N, 1, g.ldb, 0, static_cast<uint32_t>((i + 1) * b_rows / TOKEN_BOXES));
-    if (!g.b_mn) ok &= map3(&p.tm_b, g.B, g.dtype, g.K, g.N, 1, g.ldb, 0, static_cast<uint32_t>(b_rows));
+    if (!g.b_mn) ok &= map3(&p.tm_b, g.B, g.dtype, g.K, g.N, 1, g.ldb, 0, static_cast<uint32_t>(pair ? bn / 2 : bn));
     else if (p.chunked_b) ok &= map_chunked(&p.tm_b, g.B, g.dtype, wb, g.K, 1, g.ldb, 0);
     else ok &= map3(&p.tm_b, g.B, g.dtype, g.N, g.K, 1, g.ldb, 0, BK);
     const int64_t c_count = g.group == GROUP_K ? g.groups : g.splits > 1 ? g.splits : 1;
