@@ -449,9 +449,9 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
             const int half = kPair ? tile.n / 2 : tile.n;  // columns this CTA stages
             const int b0 = tile.col0 + rank * half;
             const int a2 = p.group == GROUP_M ? tile.group : 0;
-            // a tile narrower than the stage still takes its rows in one copy: a
-            // copy costs more than the neighbours' rows that it brings (boxes of
-            // 32 rows: the experts' products 6% slower)
+            // a tile narrower than the stage still takes its rows in one copy:
+            // boxes of 32 rows made the experts' products 6% slower, one box of
+            // the smallest height that fits left them as they were
             const uint32_t tx = static_cast<uint32_t>((kPair ? 2 : 1) * stage_bytes);
             for (int kb = 0; kb < tile.nk; ++kb) {
                 if (!wait_bounded(empty0 + 8 * stage, phase ^ 1u, abort_flag, p.status)) {
