@@ -352,9 +352,9 @@ muon_status_t muon_query_status(void* workspace, void* stream);
  * for the status word that muon_query_status reads: 0, MUON_ERR_TIMEOUT, or
  * MUON_ERR_INVALID_ARG when an index array held a value the call had to leave
  * out (see each call).  Every result is the same, bit for bit, from call to
- * call on the same inputs.  The calls enqueue kernels only, so they may be
- * captured into a graph once one call has run on the device outside a
- * capture. */
+ * call on the same inputs.  The calls enqueue kernels (and, where there are no
+ * tokens, a memset) only, so they may be captured into a graph once one call
+ * has run on the device outside a capture. */
 typedef enum { MUON_I32 = 0, MUON_I64 = 1 } muon_index_t;
 
 /* out[t] = scale * table[ids[t]], t < tokens: one product in fp32, rounded

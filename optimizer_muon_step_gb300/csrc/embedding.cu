@@ -154,6 +154,7 @@ constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kShareRows = 16384;  // most rows of a share
 constexpr int kShareBits = 14;
 constexpr int kWindow = 16384;     // tokens of a share placed together
+constexpr int kPlaceWarps = 16;    // place the tokens while the others write the zero rows
 
 struct SortArgs {
     const void* ids;
@@ -170,6 +171,7 @@ struct SortShared {
     int32_t next[kShareRows + 1];  // tokens of each row, then where its next one goes; the last takes idle lanes'
     int32_t token[kWindow];
     uint16_t row[kWindow];
+    uint32_t empty[kShareRows / 32];
     int32_t warp_items[kSortWarps], warp_below[kSortWarps], warp_live[kSortWarps], warp_scan[kSortWarps];
 };
 
@@ -229,9 +231,8 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __gri
         s.warp_live[warp] = live;
     }
     __syncthreads();
-    int all_items = 0, all_live = 0, base = 0, first_item = 0;
+    int all_items = 0, all_live = 0, base = 0;
     for (int w = 0; w < kSortWarps; ++w) {
-        if (w == warp) first_item = all_items;
         all_items += s.warp_items[w];
         all_live += s.warp_live[w];
         base += s.warp_below[w];
@@ -239,11 +240,11 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __gri
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.live = all_live;
     if (blockIdx.x == 0 && outside) *a.status = MUON_ERR_INVALID_ARG;
 
-    // Zero rows; then counts -> where each row's tokens begin.
-    if (a.zeros)
-        for (int r = warp; r < rows; r += kSortWarps)
-            if (s.next[r] == 0) zero_floats(a.d_table + (v0 + r) * a.dim, a.dim, lane);
-    if (all_items == 0) return;
+    // Which rows have no token; then counts -> where each row's tokens begin.
+    for (int r = threadIdx.x; r < (rows + 31) / 32 * 32; r += kSortThreads) {
+        const unsigned m = __ballot_sync(0xffffffffu, r < rows && s.next[r < rows ? r : 0] == 0);
+        if (lane == 0) s.empty[r >> 5] = m;
+    }
     __syncthreads();
     const int per = (rows + kSortThreads - 1) / kSortThreads;  // consecutive rows of a thread
     const int r0 = min(static_cast<int>(threadIdx.x) * per, rows), r1 = min(r0 + per, rows);
@@ -265,27 +266,49 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __gri
         at += n;
     }
 
-    // The share's tokens, in order, a window of them at a time.
+    __syncthreads();
+
+    if (warp >= kPlaceWarps) {
+        if (a.zeros)
+            for (int r = warp - kPlaceWarps; r < rows; r += kSortWarps - kPlaceWarps)
+                if ((s.empty[r >> 5] >> (r & 31)) & 1) zero_floats(a.d_table + (v0 + r) * a.dim, a.dim, lane);
+        return;
+    }
+    // The share's tokens, in order, a window of them at a time; each of these
+    // warps has the stretches of two of the warps above.
+    auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(32 * kPlaceWarps) : "memory"); };
+    constexpr int kStretches = kSortWarps / kPlaceWarps;
+    const int64_t p0 = warp * kStretches * stretch < a.tokens ? warp * kStretches * stretch : a.tokens;
+    const int64_t p1 = p0 + kStretches * stretch < a.tokens ? p0 + kStretches * stretch : a.tokens;
+    int first_item = 0, my_items = 0;
+    for (int w = 0; w < (warp + 1) * kStretches; ++w) {
+        if (w < warp * kStretches) first_item += s.warp_items[w];
+        else my_items += s.warp_items[w];
+    }
     for (int w0 = 0; w0 < all_items; w0 += kWindow) {
         const int n = all_items - w0 < kWindow ? all_items - w0 : kWindow;
-        __syncthreads();
         int to = first_item - w0;
-        for (int64_t t = t0; items > 0 && t < t1; t += 32) {
-            int64_t id = -1;
-            if (t + lane < t1) id = load_index(a.ids, a.ids64, t + lane);
-            const bool in = id >= v0 && id < v0 + rows && id != a.padding_idx;
-            const unsigned m = __ballot_sync(0xffffffffu, in);
-            const int i = to + __popc(m & ((1u << lane) - 1));
-            if (in && i >= 0 && i < n) {
-                s.token[i] = static_cast<int32_t>(t + lane);
-                s.row[i] = static_cast<uint16_t>(id - v0);
+        const int stop = my_items > 0 ? min(to + my_items, n) : to;  // no token of this warp's past it
+        for (int64_t t = p0 + lane; to < stop && t < p1 + lane; t += 32 * 8) {
+            int64_t id[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) id[k] = t + 32 * k < p1 ? load_index(a.ids, a.ids64, t + 32 * k) : -1;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const bool in = id[k] >= v0 && id[k] < v0 + rows && id[k] != a.padding_idx;
+                const unsigned m = __ballot_sync(0xffffffffu, in);
+                const int i = to + __popc(m & ((1u << lane) - 1));
+                if (in && i >= 0 && i < n) {
+                    s.token[i] = static_cast<int32_t>(t + 32 * k);
+                    s.row[i] = static_cast<uint16_t>(id[k] - v0);
+                }
+                to += __popc(m);
             }
-            to += __popc(m);
         }
-        __syncthreads();
-        // 1024 at a time: each warp finds its equal rows by one ballot per bit,
+        sync();
+        // 512 at a time: each warp finds its equal rows by one ballot per bit,
         // then the warps take their places in turn
-        for (int g = 0; g < n; g += kSortThreads) {
+        for (int g = 0; g < n; g += 32 * kPlaceWarps) {
             const int i = g + threadIdx.x;
             const int row = i < n ? s.row[i] : rows;
             unsigned same = 0xffffffffu;
@@ -297,7 +320,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __gri
                 same &= one ? m : ~m;
             }
             const int rank = __popc(same & ((1u << lane) - 1));
-            const int turns = n - g < kSortThreads ? (n - g + 31) / 32 : kSortWarps;
+            const int turns = min((n - g + 31) / 32, kPlaceWarps);
             for (int w = 0; w < turns; ++w) {
                 if (w == warp) {
                     const int first = s.next[row];
@@ -308,7 +331,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __gri
                         a.pos[first + rank] = s.token[i];
                     }
                 }
-                __syncthreads();
+                sync();
             }
         }
     }
