@@ -734,8 +734,9 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
                 }
             }
         }
-        // the output stores complete before the CTA exits
-        if (lane == 0) bulk_wait_all();
+        // the output stores have read shared memory before the CTA exits; the
+        // kernel's end waits for their writes
+        if (lane == 0) bulk_wait_read<0>();
         __syncwarp();
     }
 
