@@ -276,24 +276,62 @@ __device__ __forceinline__ void store_rows(const GemmParams& p, const uint8_t* b
     }
 }
 
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+
+__device__ __forceinline__ float2 unpack2(uint64_t x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 // Softmax sums of one row of a tile, base 2: after all columns, sum =
 // sum exp2(x - top), x = logit * log2(e) * logit_scale, the target's column
-// left out (its logit is computed apart, see cross_entropy.cu).
+// left out (its logit is computed apart, see cross_entropy.cu).  Pairs of
+// columns share the multiply-adds and the sums, in four chains: at K = 1000 a
+// tile's products take no longer than its epilogue.
 struct RowSums {
     float top, sum;
-    __device__ __forceinline__ void add(const float (&x)[32]) {
-        float m = x[0];
+    // x = scale * v, scale > 0
+    __device__ __forceinline__ void add(const float (&v)[32], float scale) {
+        float m[4];
 #pragma unroll
-        for (int i = 1; i < 32; ++i) m = fmaxf(m, x[i]);
-        m = fmaxf(m, top);
+        for (int i = 0; i < 4; ++i) m[i] = fmaxf(fmaxf(v[i], v[4 + i]), v[8 + i]);
+#pragma unroll
+        for (int k = 12; k < 32; k += 4)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m[i] = fmaxf(m[i], v[k + i]);
+        const float most = fmaxf(scale * fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), top);
         // an infinite maximum is not subtracted: inf - inf would be NaN where
         // the sum is inf, and -inf leaves the sum at 0
-        const float ref = isinf(m) ? 0.f : m;
-        float s = top == -INFINITY ? 0.f : sum * ex2((isinf(top) ? 0.f : top) - ref);
+        const float ref = isinf(most) ? 0.f : most;
+        const uint64_t s2 = pack2(scale, scale), r2 = pack2(-ref, -ref);
+        uint64_t part[2] = {pack2(top == -INFINITY ? 0.f : sum * ex2((isinf(top) ? 0.f : top) - ref), 0.f), pack2(0.f, 0.f)};
 #pragma unroll
-        for (int i = 0; i < 32; ++i) s += ex2(x[i] - ref);
-        top = m;
-        sum = s;
+        for (int k = 0; k < 32; k += 4)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float2 x = unpack2(fma2(pack2(v[k + 2 * i], v[k + 2 * i + 1]), s2, r2));
+                part[i] = add2(part[i], pack2(ex2(x.x), ex2(x.y)));
+            }
+        const float2 s = unpack2(add2(part[0], part[1]));
+        top = most;
+        sum = s.x + s.y;
     }
 };
 
@@ -656,8 +694,10 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
                             bulk_commit();
                         }
                     }
+                    if (p.ce.scale2 <= 0.f) {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) v[k] *= p.ce.scale2;
+                        for (int k = 0; k < 32; ++k) v[k] *= p.ce.scale2;
+                    }
                     const int off = target - col;
                     if (__any_sync(0xffffffffu, off >= 0 && off < 32)) {
 #pragma unroll
@@ -669,7 +709,7 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
                         for (int k = 0; k < 32; ++k)
                             if (col + k >= p.N) v[k] = -INFINITY;
                     }
-                    rs.add(v);
+                    rs.add(v, p.ce.scale2 > 0.f ? p.ce.scale2 : 1.f);
                 }
                 if (row < tile.rows_end && row + lane < p.M)
                     p.ce.sums[(static_cast<int64_t>(row + lane) * p.tiles_n + tile.tn) * 2 + half] = make_float2(rs.top, rs.sum);

@@ -354,6 +354,18 @@ def test_cross_entropy_large_logits_and_overflow(lib, dtype):
     assert not torch.isfinite(lse2[7])
 
 
+@pytest.mark.parametrize("scale", [-0.7, 0.0, 1e-6])
+def test_cross_entropy_other_logit_scales(lib, scale):
+    """Negative, zero and tiny logit scales, with an odd vocabulary."""
+    hidden, weight, targets = ce_inputs(55, 90, 333, 72, BF, ignored=0.1)
+    want = ce_want(hidden, weight, targets, None, scale, -100)
+    loss, lse, dh, dw = m.muon_linear_ce_grad(hidden, weight, targets, logit_scale=scale)
+    within(loss, want["loss"], want["loss_bound"], "loss")
+    within(lse, want["lse"], want["lse_bound"], "lse")
+    within(dh, want["dh"], rounded(want["bh"], want["dh"], BF), "d_hidden")
+    within(dw, want["dw"], rounded(want["bw"], want["dw"], BF), "d_weight")
+
+
 def test_cross_entropy_small_gradients_in_fp16(lib):
     """Row scales of 1e-7 would put every fp16 logit gradient below the type's
     subnormals; the rounding is relative to the largest scale instead."""
