@@ -113,8 +113,8 @@ struct TrainGemm {
 };
 cudaError_t train_gemm(const TrainGemm& g, int num_sms, cudaStream_t st);
 size_t train_gemm_group_bytes(int64_t groups);
-int64_t train_gemm_sums(int64_t M, int64_t N);     // softmax sums per row: two per column tile
-int64_t train_gemm_max_sums(int64_t N);            // whatever M is
+int64_t train_gemm_sums(int64_t M, int64_t N, int64_t K);  // softmax sums per row: two per column tile
+int64_t train_gemm_max_sums(int64_t N);                    // whatever M and K are
 int64_t train_gemm_tiles(int64_t M, int64_t N);    // tiles of a plain product, one per CTA or CTA pair
 // out = alpha * the sum of `splits` fp32 matrices, in order.
 cudaError_t launch_split_sum(const float* parts, int64_t ld, int64_t stride, int splits, float alpha,

@@ -337,7 +337,7 @@ muon_status_t ce_run(const muon_linear_ce_t* p, bool grad, void* workspace, size
         c.vocab = v;
         c.dim = d;
         c.ignore_index = p->ignore_index;
-        c.row_sums = train_gemm_sums(m, v);
+        c.row_sums = train_gemm_sums(m, v, d);
         c.targets64 = p->targets_dtype == MUON_I64;
         c.dtype = p->dtype;
         c.logit_scale = p->logit_scale;

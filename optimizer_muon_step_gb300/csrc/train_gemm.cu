@@ -62,7 +62,12 @@ constexpr int MAX_STAGES = 12;
 constexpr int SMEM_BYTES = 1024 + RING_BYTES + EBUFS_BYTES + 1024;
 
 // What a product's tiles end in.
-enum { END_STORE = 0, END_CE = 1, END_TOKENS = 2 };
+// The LONG ones cut the sum over K into segments (see the epilogue).
+// Terms summed by the tensor core in one go: 1024 where 32 bits of the sum
+// count (2e-6 off at 2048, 9e-6 at 8192), 16384 (2e-5) where the result is
+// rounded to 16 bits.
+constexpr int kExactTerms = 1024, kRoundedTerms = 16384;
+enum { END_STORE = 0, END_CE = 1, END_TOKENS = 2, END_STORE_LONG = 3, END_CE_LONG = 4, ENDS = 5 };
 
 struct GemmParams {
     CUtensorMap tm_a, tm_b, tm_c;
@@ -78,6 +83,7 @@ struct GemmParams {
     int32_t tiles_m, tiles_n, total_tiles;  // GROUP_M: tiles_n and total_tiles are found on the device
     int32_t bn;                     // columns of a tile, a multiple of 32 (64 for 16-bit C) up to BN
     int32_t stages;                 // of the ring
+    int32_t segment;                // k-blocks summed by the tensor core in one go
     int32_t a_bytes, b_bytes;       // of a stage
     int32_t band;                   // rows of tiles walked together (GROUP_NONE, GROUP_K)
     int32_t groups, group, offsets64;
@@ -232,7 +238,7 @@ __device__ __forceinline__ float ex2(float x) {
 
 // 2 N fp32 values rounded to 16 bits, in pairs.
 template <int N>
-__device__ __forceinline__ void pack_row(const float (&v)[2 * N], uint32_t (&w)[N], int dtype) {
+__device__ __forceinline__ void pack_row(const float (&v)[2 * N], uint32_t* w, int dtype) {
     if (dtype == MUON_BF16) {
 #pragma unroll
         for (int k = 0; k < N; ++k) {
@@ -288,9 +294,9 @@ __device__ __forceinline__ float2 unpack2(uint64_t x) {
     return r;
 }
 
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
 
@@ -303,32 +309,32 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 // Softmax sums of one row of a tile, base 2: after all columns, sum =
 // sum exp2(x - top), x = logit * log2(e) * logit_scale, the target's column
 // left out (its logit is computed apart, see cross_entropy.cu).  Pairs of
-// columns share the multiply-adds and the sums, in four chains: at K = 1000 a
-// tile's products take no longer than its epilogue.
+// columns share the arithmetic, in independent chains.
 struct RowSums {
     float top, sum;
-    // x = scale * v, scale > 0
-    __device__ __forceinline__ void add(const float (&v)[32], float scale) {
-        float m[4];
+    // adds the columns of v whose bit in `out` is clear
+    __device__ __forceinline__ void add(float (&v)[32], float scale, uint32_t out) {
+        const uint64_t s2 = pack2(scale, scale);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) m[i] = fmaxf(fmaxf(v[i], v[4 + i]), v[8 + i]);
+        for (int k = 0; k < 32; k += 2) {
+            const float2 x = unpack2(mul2(pack2(v[k], v[k + 1]), s2));
+            v[k] = (out >> k) & 1 ? -INFINITY : x.x;
+            v[k + 1] = (out >> (k + 1)) & 1 ? -INFINITY : x.y;
+        }
+        float m[4] = {top, v[0], v[1], v[2]};
 #pragma unroll
-        for (int k = 12; k < 32; k += 4)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) m[i] = fmaxf(m[i], v[k + i]);
-        const float most = fmaxf(scale * fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), top);
+        for (int k = 3; k < 32; ++k) m[k & 3] = fmaxf(m[k & 3], v[k]);
+        const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
         // an infinite maximum is not subtracted: inf - inf would be NaN where
         // the sum is inf, and -inf leaves the sum at 0
         const float ref = isinf(most) ? 0.f : most;
-        const uint64_t s2 = pack2(scale, scale), r2 = pack2(-ref, -ref);
+        const uint64_t r2 = pack2(-ref, -ref);
         uint64_t part[2] = {pack2(top == -INFINITY ? 0.f : sum * ex2((isinf(top) ? 0.f : top) - ref), 0.f), pack2(0.f, 0.f)};
 #pragma unroll
-        for (int k = 0; k < 32; k += 4)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float2 x = unpack2(fma2(pack2(v[k + 2 * i], v[k + 2 * i + 1]), s2, r2));
-                part[i] = add2(part[i], pack2(ex2(x.x), ex2(x.y)));
-            }
+        for (int k = 0; k < 32; k += 2) {
+            const float2 x = unpack2(add2(pack2(v[k], v[k + 1]), r2));
+            part[(k >> 1) & 1] = add2(part[(k >> 1) & 1], pack2(ex2(x.x), ex2(x.y)));
+        }
         const float2 s = unpack2(add2(part[0], part[1]));
         top = most;
         sum = s.x + s.y;
@@ -359,7 +365,8 @@ __device__ __forceinline__ void write_scalars(const CeEpilogue& ce, int lane) {
 
 template <bool kPair, int kEnd>
 __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
-    constexpr bool kCe = kEnd == END_CE;
+    constexpr bool kCe = kEnd == END_CE || kEnd == END_CE_LONG;
+    constexpr bool kLong = kEnd == END_CE_LONG || kEnd == END_STORE_LONG;
     constexpr int TILE_M = kPair ? 2 * BM : BM;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -519,7 +526,7 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
                     const int k = tile.k0 + kb * BK;
                     if (p.a_mn) load_mn(sa, ma, p.chunked_a, row, BM / 64, k, a2);
                     else load3(sa, ma, k, row, a2);
-                    if (p.b_mn) load_mn(sb, mb, p.chunked_b, b0, (kPair ? BN / 2 : BN) / 64, k, 0);
+                    if (p.b_mn) load_mn(sb, mb, p.chunked_b, b0, (kPair ? p.bn / 2 : p.bn) / 64, k, 0);
                     else load3(sb, mb, k, b0, 0);
                 }
                 ++issued;
@@ -547,36 +554,37 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
         const uint64_t step_a = p.a_mn ? 16 * 128 / 16 : 32 / 16, step_b = p.b_mn ? 16 * 128 / 16 : 32 / 16;
         for (int i = 0; ok && read_tile(i, tile); ++i) {
             if (tile.nk == 0) continue;
-            const int acc = local & 1;
-            const uint32_t acc_phase = static_cast<uint32_t>(local >> 1) & 1u;
-            ok = wait_bounded(smem_u32(&tempty_bar[acc]), acc_phase ^ 1u, abort_flag, p.status);
-            tc_fence_after();
             const uint32_t idesc = p.idesc | (static_cast<uint32_t>(tile.n >> 3) << 17) |
                                    (static_cast<uint32_t>(TILE_M >> 4) << 24);
-            const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
-            for (int kb = 0; ok && kb < tile.nk; ++kb) {
-                if (!wait_bounded(full0 + 8 * stage, phase, abort_flag, p.status)) {
-                    ok = false;
-                    break;
-                }
+            for (int k0 = 0; ok && k0 < tile.nk; k0 += p.segment, ++local) {
+                const int acc = local & 1;
+                const uint32_t acc_phase = static_cast<uint32_t>(local >> 1) & 1u;
+                const int k1 = min(k0 + p.segment, tile.nk);
+                ok = wait_bounded(smem_u32(&tempty_bar[acc]), acc_phase ^ 1u, abort_flag, p.status);
                 tc_fence_after();
-                const uint64_t at = static_cast<uint32_t>(stage * stage_bytes) >> 4;
-                if (elected)  // the tile's first MMA overwrites the accumulator
-                    tc_mma_k_block<kPair>(d_tmem, desc_a + at, desc_b + at, idesc, kb > 0 ? 1u : 0u, step_a, step_b);
-                if (elected) {
-                    if (kPair) tc_commit_pair_mc(empty0 + 8 * stage, 0x3);
-                    else tc_commit(empty0 + 8 * stage);
+                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
+                for (int kb = k0; ok && kb < k1; ++kb) {
+                    if (!wait_bounded(full0 + 8 * stage, phase, abort_flag, p.status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t at = static_cast<uint32_t>(stage * stage_bytes) >> 4;
+                    if (elected) {  // the segment's first MMA overwrites the accumulator
+                        tc_mma_k_block<kPair>(d_tmem, desc_a + at, desc_b + at, idesc, kb > k0 ? 1u : 0u, step_a, step_b);
+                        if (kPair) tc_commit_pair_mc(empty0 + 8 * stage, 0x3);
+                        else tc_commit(empty0 + 8 * stage);
+                    }
+                    if (++stage == p.stages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
                 }
-                if (++stage == p.stages) {
-                    stage = 0;
-                    phase ^= 1u;
+                if (ok && elected) {
+                    if (kPair) tc_commit_pair_mc(smem_u32(&tfull_bar[acc]), 0x3);
+                    else tc_commit(smem_u32(&tfull_bar[acc]));
                 }
             }
-            if (ok && elected) {
-                if (kPair) tc_commit_pair_mc(smem_u32(&tfull_bar[acc]), 0x3);
-                else tc_commit(smem_u32(&tfull_bar[acc]));
-            }
-            ++local;
         }
         // drain: all issued MMAs complete before TMEM is released
         if (elected) {
@@ -595,28 +603,29 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
         int local = 0;
         const float alpha = p.alpha_dev ? p.alpha * *p.alpha_dev : p.alpha;
         if (kCe && !kPair && p.ce.first && blockIdx.x == 0 && warp == 2) write_scalars(p.ce, lane);
-        for (int i = 0; read_tile(i, tile); ++i) {
-            const int acc = local & 1;
-            const uint32_t acc_phase = static_cast<uint32_t>(local >> 1) & 1u;
+        bool ok = true;
+        for (int i = 0; ok && read_tile(i, tile); ++i) {
             const int row = tile.row0 + rank * BM + quarter * 32;
             const bool live = tile.nk > 0;
-            if (live) {
-                if (!wait_bounded(smem_u32(&tfull_bar[acc]), acc_phase, abort_flag, p.status)) break;
+            // The next segment's accumulator: waits until it is complete; its
+            // address for this warp's lanes.
+            auto next_segment = [&]() -> uint32_t {
+                const int acc = local & 1;
+                ok = wait_bounded(smem_u32(&tfull_bar[acc]), static_cast<uint32_t>(local >> 1) & 1u, abort_flag, p.status);
                 tc_fence_after();
-                ++local;
-            }
-            const uint32_t t_addr = tmem_base + static_cast<uint32_t>(acc * BN) + (static_cast<uint32_t>(quarter * 32) << 16);
-            // this warp has read its last of the accumulator: handed back before
-            // the last block is stored, and without waiting for stores
-            // (2048-row experts of 512 tokens: a release after them took 3400 of
-            // 6900 cycles a tile)
+                return tmem_base + static_cast<uint32_t>(acc * BN) + (static_cast<uint32_t>(quarter * 32) << 16);
+            };
+            // This warp has read its last of the accumulator: handed back before
+            // anything is stored, and without waiting for stores (2048-row
+            // experts of 512 tokens: a release after them took 3400 of 6900
+            // cycles a tile).
             auto release = [&]() {
-                if (!live) return;
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
+                const int acc = local & 1;
+                if (lane == 0)
                     mbar_arrive_cluster_relaxed(kPair ? mapa_shared(smem_u32(&tempty_bar[acc]), 0) : smem_u32(&tempty_bar[acc]));
-                }
+                ++local;
             };
             // the block buffer is free again once its last tensor store has read it
             auto claim = [&]() {
@@ -631,16 +640,18 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
                 // last tokens are stored one by one.
                 const int cols = tile.cols_end - tile.col0;
                 const bool mine = row < tile.rows_end && 32 * half < cols;
-                if (!mine) release();
+                const uint32_t t_addr = live ? next_segment() : 0;
+                if (!ok) break;
+                if (!mine && live) release();
                 for (int c = 32 * half; mine && c < cols; c += 64) {
                     float v[32];
                     if (live) {
                         tmem_load_32cols(t_addr + static_cast<uint32_t>(c), v);
+                        if (c + 64 >= cols) release();
                     } else {
 #pragma unroll
                         for (int k = 0; k < 32; ++k) v[k] = 0.f;
                     }
-                    if (c + 64 >= cols) release();
                     uint32_t w[16];
                     pack_row<16>(v, w, p.c_dtype);
                     if (p.tma_c && c + 32 <= cols) {
@@ -664,105 +675,29 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
                             if (c + k < cols) *o = static_cast<uint16_t>(k & 1 ? w[k / 2] >> 16 : w[k / 2]);
                     }
                 }
-            } else if (kCe) {
-                // the tile's halves of the columns, in steps of 32
-                const int mid = (p.bn / 2 + 31) & ~31, lo = half ? mid : 0, hi = half ? p.bn : mid;
-                const bool mine = row < tile.rows_end && tile.col0 + lo < p.N;
-                if (!mine) release();
+            } else {
+                // this warp's columns of the tile, up to 128 from `lo` on
+                const int mid = (p.bn / 2 + 31) & ~31;
+                const int lo = half ? mid : 0;
+                const int cols = min((half ? p.bn : mid) - lo, p.N - tile.col0 - lo);
+                // an empty group adds nothing
+                const bool mine = row < tile.rows_end && cols > 0 && (live || !p.accumulate);
+                const bool wide = p.c_dtype == MUON_F32;
+
                 RowSums rs = {-INFINITY, 0.f};
                 int target = -1;
-                if (mine && row + lane < p.M) {
+                if (kCe && mine && row + lane < p.M) {
                     const int64_t tg = load_index(p.ce.targets, p.ce.targets64, row + lane);
                     target = tg >= 0 && tg < p.N ? static_cast<int>(tg) : -1;
                 }
-                for (int c = lo; mine && c < hi && tile.col0 + c < p.N; c += 32) {
-                    const int col = tile.col0 + c;
-                    float v[32];
-                    tmem_load_32cols(t_addr + static_cast<uint32_t>(c), v);
-                    if (c + 32 >= hi || col + 32 >= p.N) release();
-                    if (p.ce.store) {
-                        claim();
-                        uint8_t* brow = buf + lane * 128;
-#pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            *reinterpret_cast<float4*>(brow + ((q ^ sw) << 4)) =
-                                make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                // a finished block: out of shared memory to C at column c of this warp's
+                auto put = [&](int c) {
+                    const int col = tile.col0 + lo + c;
+                    if (kCe || p.tma_c) {  // logits' rows are the library's, on 256 bytes
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
-                            tma_store_3d(&p.tm_c, smem_u32(buf), col, row, 0);
-                            bulk_commit();
-                        }
-                    }
-                    if (p.ce.scale2 <= 0.f) {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) v[k] *= p.ce.scale2;
-                    }
-                    const int off = target - col;
-                    if (__any_sync(0xffffffffu, off >= 0 && off < 32)) {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (k == off) v[k] = -INFINITY;
-                    }
-                    if (col + 32 > p.N) {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (col + k >= p.N) v[k] = -INFINITY;
-                    }
-                    rs.add(v, p.ce.scale2 > 0.f ? p.ce.scale2 : 1.f);
-                }
-                if (row < tile.rows_end && row + lane < p.M)
-                    p.ce.sums[(static_cast<int64_t>(row + lane) * p.tiles_n + tile.tn) * 2 + half] = make_float2(rs.top, rs.sum);
-            } else {
-                // the tile's halves of 128 columns, in blocks of 128 bytes a
-                // row; an empty group adds nothing
-                const int cols = p.c_dtype == MUON_F32 ? 32 : 64;
-                const int lo = half * (BN / 2), hi = min(lo + BN / 2, p.N - tile.col0);
-                const bool mine = row < tile.rows_end && lo < hi && (live || !p.accumulate);
-                if (!mine) release();
-                for (int c = lo; mine && c < hi; c += cols) {
-                    const int col = tile.col0 + c;
-                    uint8_t* brow = buf + lane * 128;
-                    if (cols == 32) {
-                        float v[32];
-                        if (live) {
-                            tmem_load_32cols(t_addr + static_cast<uint32_t>(c), v);
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) v[k] = 0.f;
-                        }
-                        if (c + cols >= hi) release();
-                        claim();
-#pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            *reinterpret_cast<float4*>(brow + ((q ^ sw) << 4)) = make_float4(
-                                alpha * v[4 * q], alpha * v[4 * q + 1], alpha * v[4 * q + 2], alpha * v[4 * q + 3]);
-                    } else {
-                        float v[64];
-                        if (live) {
-                            tmem_load_64cols(t_addr + static_cast<uint32_t>(c), v);
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 64; ++k) v[k] = 0.f;
-                        }
-                        if (c + cols >= hi) release();
-                        if (alpha != 1.f) {
-#pragma unroll
-                            for (int k = 0; k < 64; ++k) v[k] *= alpha;
-                        }
-                        uint32_t w[32];
-                        pack_row<32>(v, w, p.c_dtype);
-                        claim();
-#pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            *reinterpret_cast<uint4*>(brow + ((q ^ sw) << 4)) =
-                                make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-                    }
-                    if (p.tma_c) {
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            if (p.accumulate) tma_add_3d(&p.tm_c, smem_u32(buf), col, row, tile.c2);
+                            if (!kCe && p.accumulate) tma_add_3d(&p.tm_c, smem_u32(buf), col, row, tile.c2);
                             else tma_store_3d(&p.tm_c, smem_u32(buf), col, row, tile.c2);
                             bulk_commit();
                         }
@@ -771,7 +706,125 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
                         store_rows(p, buf, row, tile.rows_end, col, tile.c2, lane);
                         __syncwarp();
                     }
+                };
+                // 32 columns of fp32, or 64 packed in pairs, as a block of 128 bytes a row
+                auto put_wide = [&](const float(&v)[32], int c) {
+                    claim();
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        *reinterpret_cast<float4*>(buf + lane * 128 + ((q ^ sw) << 4)) =
+                            make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                    put(c);
+                };
+                auto put_pairs = [&](const uint32_t(&w)[32], int c) {
+                    claim();
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        *reinterpret_cast<uint4*>(buf + lane * 128 + ((q ^ sw) << 4)) =
+                            make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+                    put(c);
+                };
+                // 32 columns of logits from column c of this warp's
+                auto put_logits = [&](float(&v)[32], int c) {
+                    if (p.ce.store) put_wide(v, c);
+                    // left out: the target's column, and those past the edge
+                    const int off = target - (tile.col0 + lo + c);
+                    const uint32_t out = (off >= 0 && off < 32 ? 1u << off : 0u) | (c + 32 > cols ? ~0u << (cols - c) : 0u);
+                    rs.add(v, p.ce.scale2, out);
+                };
+
+                if (kLong) {
+                    // The tensor core's accumulator truncates, which is off by about
+                    // 1e-9 of the result per term of the sum.  Long sums are cut into
+                    // segments, added here with proper rounding, in registers.
+                    constexpr int kChunks = kPair ? 4 : 2;  // of 32 columns: half a tile
+                    float acc[kChunks][32];
+#pragma unroll
+                    for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) acc[c][k] = 0.f;
+                    for (int k0 = 0; ok && k0 < tile.nk; k0 += p.segment) {
+                        const uint32_t t_addr = next_segment() + static_cast<uint32_t>(lo);
+                        if (!ok) break;
+#pragma unroll
+                        for (int c = 0; c < kChunks; ++c) {
+                            if (mine && 32 * c < cols) {
+                                float v[32];
+                                tmem_load_32cols(t_addr + 32 * c, v);
+#pragma unroll
+                                for (int k = 0; k < 32; k += 2) {
+                                    const float2 s = unpack2(add2(pack2(acc[c][k], acc[c][k + 1]), pack2(v[k], v[k + 1])));
+                                    acc[c][k] = s.x;
+                                    acc[c][k + 1] = s.y;
+                                }
+                            }
+                        }
+                        release();
+                    }
+                    if (!ok) break;
+                    if (!kCe && alpha != 1.f) {
+#pragma unroll
+                        for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) acc[c][k] *= alpha;
+                    }
+#pragma unroll
+                    for (int c = 0; c < kChunks; ++c) {
+                        if (!mine || 32 * c >= cols) continue;
+                        if (kCe) {
+                            put_logits(acc[c], 32 * c);
+                        } else if (wide) {
+                            put_wide(acc[c], 32 * c);
+                        } else if ((c & 1) == 0) {
+                            uint32_t w[32];
+                            pack_row<16>(acc[c], w, p.c_dtype);
+                            pack_row<16>(acc[c + 1 < kChunks ? c + 1 : c], w + 16, p.c_dtype);
+                            put_pairs(w, 32 * c);
+                        }
+                    }
+                } else {
+                    const uint32_t t_addr = live ? next_segment() + static_cast<uint32_t>(lo) : 0;
+                    if (!ok) break;
+                    if (!mine && live) release();
+                    const int step = wide ? 32 : 64;
+                    for (int c = 0; mine && c < cols; c += step) {
+                        if (wide) {
+                            float v[32];
+                            if (live) {
+                                tmem_load_32cols(t_addr + static_cast<uint32_t>(c), v);
+                                if (c + step >= cols) release();
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) v[k] = 0.f;
+                            }
+                            if (kCe) {
+                                put_logits(v, c);
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) v[k] *= alpha;
+                                put_wide(v, c);
+                            }
+                        } else if (!kCe) {
+                            float v[64];
+                            if (live) {
+                                tmem_load_64cols(t_addr + static_cast<uint32_t>(c), v);
+                                if (c + step >= cols) release();
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < 64; ++k) v[k] = 0.f;
+                            }
+                            if (alpha != 1.f) {
+#pragma unroll
+                                for (int k = 0; k < 64; ++k) v[k] *= alpha;
+                            }
+                            uint32_t w[32];
+                            pack_row<32>(v, w, p.c_dtype);
+                            put_pairs(w, c);
+                        }
+                    }
                 }
+                if (kCe && row < tile.rows_end && row + lane < p.M)
+                    p.ce.sums[(static_cast<int64_t>(row + lane) * p.tiles_n + tile.tn) * 2 + half] = make_float2(rs.top, rs.sum);
             }
         }
         // the output stores have read shared memory before the CTA exits; the
@@ -942,13 +995,15 @@ bool map_chunked(CUtensorMap* map, const void* base, int dtype, int64_t inner, i
 typedef void (*GemmKernel)(const GemmParams);
 
 GemmKernel single_kernel(int end) {
-    return end == END_CE ? train_gemm_kernel<END_CE> : end == END_TOKENS ? train_gemm_kernel<END_TOKENS> : train_gemm_kernel<END_STORE>;
+    static const GemmKernel k[ENDS] = {train_gemm_kernel<0>, train_gemm_kernel<1>, train_gemm_kernel<2>,
+                                       train_gemm_kernel<3>, train_gemm_kernel<4>};
+    return k[end];
 }
 
 GemmKernel pair_kernel(int end) {
-    return end == END_CE       ? train_gemm_pair_kernel<END_CE>
-           : end == END_TOKENS ? train_gemm_pair_kernel<END_TOKENS>
-                               : train_gemm_pair_kernel<END_STORE>;
+    static const GemmKernel k[ENDS] = {train_gemm_pair_kernel<0>, train_gemm_pair_kernel<1>, train_gemm_pair_kernel<2>,
+                                       train_gemm_pair_kernel<3>, train_gemm_pair_kernel<4>};
+    return k[end];
 }
 
 // Kernel attributes and the pair occupancy, set up once per device (with
@@ -967,7 +1022,7 @@ cudaError_t setup(int* max_pairs) {
     if (!done[dev]) {
         const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
         cudaError_t e = cudaSuccess;
-        for (int end = END_STORE; end <= END_TOKENS && e == cudaSuccess; ++end) {
+        for (int end = 0; end < ENDS && e == cudaSuccess; ++end) {
             e = cudaFuncSetAttribute(single_kernel(end), attr, SMEM_BYTES);
             if (e == cudaSuccess) e = cudaFuncSetAttribute(pair_kernel(end), attr, SMEM_BYTES);
         }
@@ -1006,8 +1061,9 @@ size_t train_gemm_group_bytes(int64_t groups) { return static_cast<size_t>(group
 // With more than 128 rows the product is bound by the MMAs, and narrower tiles
 // lose more by their edges than the last wave costs (999 x 32003, K = 1000: 79
 // us at 192 columns, 67 at 256).
-int64_t train_gemm_bn(int64_t M, int64_t N) {
+int64_t train_gemm_bn(int64_t M, int64_t N, int64_t K) {
     if (M > BM) return BN;
+    if (K > kExactTerms) return BN / 2;
     int64_t best = BN, cost = 0;
     for (int64_t bn = BN; bn >= 128; bn -= 32) {
         const int64_t waves = ((N + bn - 1) / bn + 151) / 152;
@@ -1020,8 +1076,8 @@ int64_t train_gemm_bn(int64_t M, int64_t N) {
     return best;
 }
 
-int64_t train_gemm_sums(int64_t M, int64_t N) {
-    const int64_t bn = train_gemm_bn(M, N);
+int64_t train_gemm_sums(int64_t M, int64_t N, int64_t K) {
+    const int64_t bn = train_gemm_bn(M, N, K);
     return 2 * ((N + bn - 1) / bn);
 }
 
@@ -1034,11 +1090,21 @@ cudaError_t train_gemm(const TrainGemm& g, int num_sms, cudaStream_t st) {
     const bool pair = use_pairs(g);
     GemmParams p;
     memset(&p, 0, sizeof p);
-    const int end = g.ce.sums ? END_CE : g.group == GROUP_M ? END_TOKENS : END_STORE;
+    // a group's share of K is not known here: twice the average is assumed
+    const bool exact = g.ce.sums || (g.c_dtype == MUON_F32 && g.splits <= 1);
+    const int64_t terms = g.group == GROUP_K ? 2 * g.K / g.groups : g.splits > 1 ? g.K / g.splits : g.K;
+    const bool longer = g.group != GROUP_M && terms > (exact ? kExactTerms : kRoundedTerms);
+    const int end = g.group == GROUP_M ? END_TOKENS
+                    : g.ce.sums        ? (longer ? END_CE_LONG : END_CE)
+                                       : (longer ? END_STORE_LONG : END_STORE);
     const int64_t a_count = g.group == GROUP_M ? g.groups : 1;
     int64_t bn = BN;
-    if (end == END_CE) {
-        bn = train_gemm_bn(g.M, g.N);
+    // a single CTA's long sums stay in 64 registers a thread: with 128 the
+    // kernel takes all of an SM's registers, and its launch no longer overlaps
+    // the kernel before it (16 tokens against 163840 x 2048: 6 us)
+    if (longer && !pair) bn = BN / 2;
+    if (g.ce.sums) {
+        bn = train_gemm_bn(g.M, g.N, g.K);
     } else if (end == END_TOKENS) {
         // about the tokens of two average experts, so that few experts need two tiles
         const int64_t want = 2 * ((g.N + g.groups - 1) / g.groups);
@@ -1094,6 +1160,7 @@ cudaError_t train_gemm(const TrainGemm& g, int num_sms, cudaStream_t st) {
     p.a_mn = g.a_mn;
     p.b_mn = g.b_mn;
     p.alpha = g.alpha;
+    p.segment = !longer ? INT32_MAX / 2 : (exact ? kExactTerms : kRoundedTerms) / BK;
     p.idesc = (1u << 4) | (g.dtype == MUON_BF16 ? (1u << 7) | (1u << 10) : 0u) | ((g.a_mn ? 1u : 0u) << 15) |
               ((g.b_mn ? 1u : 0u) << 16);
     const int64_t kb = (g.K + BK - 1) / BK;
