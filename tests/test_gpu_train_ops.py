@@ -252,6 +252,34 @@ def test_cross_entropy_and_gradients(lib, dtype, n, v, d):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("n,v,d", [(100, 900, 1400), (200, 1500, 2056), (1100, 100, 72), (1100, 400, 72), (1800, 20000, 2048),
+                                   (128, 100000, 7168)])
+def test_cross_entropy_long_sums(lib, n, v, d):
+    """Sums that are cut into segments: over the width (logits, above 1024),
+    over the tokens (an fp32 d_weight, above 1024) and over the vocabulary
+    (d_hidden, above 16384 a piece), with up to 128 rows and more."""
+    hidden, weight, targets = ce_inputs(n + v + 1, n, v, d, HF, ignored=0.1)
+    scale = torch.rand(n, generator=gen(n), device=DEV) / n
+    want = ce_want(hidden, weight, targets, scale, 1.0, -100)
+    dw = torch.empty(v, d, device=DEV)
+    loss, lse, dh, _ = m.muon_linear_ce_grad(hidden, weight, targets, row_scale=scale, d_weight=dw)
+    within(loss, want["loss"], want["loss_bound"], "loss")
+    within(lse, want["lse"], want["lse_bound"], "lse")
+    within(dh, want["dh"], rounded(want["bh"], want["dh"], HF), "d_hidden")
+    within(dw, want["dw"], want["bw"], "d_weight")
+    # segments keep the truncation of the tensor core's sums at that of their
+    # 1024 terms, 2^-23 a MMA of 16 or 64 * 2^-23 of the result at most, and
+    # the fp32 additions of 8 segments, exponentials and logarithm below 2^-20
+    assert ((lse.double() - want["lse"]).norm() / want["lse"].norm()).item() < 64 * 2.0 ** -23
+
+
+def test_expert_wgrad_long_sums(lib):
+    """fp32 gradients over more than 1024 tokens an expert, few and many rows."""
+    for rows in (96, 264):
+        x, dy, w, off = expert_case(rows, split(4, 4000, 3), rows, 200, BF)
+        expert_check(x, dy, w, off, BF)
+
+
 @pytest.mark.parametrize("dtype", [BF, HF])
 def test_cross_entropy_in_blocks_of_tokens(lib, dtype):
     """A workspace that holds 256 tokens: the gradient of the weights is summed
