@@ -178,9 +178,9 @@ namespace {
 // hidden rows, and with gradients the rows
 // of logits and the pieces of d_hidden.
 struct CeLayout {
-    int64_t block = 0;   // tokens per block
     int64_t z_ld = 0, h_ld = 0, w_ld = 0, part_ld = 0;
     int splits = 1;      // pieces of the vocabulary in d_hidden's product
+    int last_splits = 1; // and in that of a shorter last block
     bool pack_w = false, pack_h = false, sums = false;
     size_t w_off = 0, sum_off = 0, tile_off = 0, h_off = 0, z_off = 0, part_off = 0, total = 0;
 };
@@ -219,7 +219,6 @@ size_t ce_total(const muon_linear_ce_t* p, bool grad, int64_t block, CeLayout* L
         at += static_cast<size_t>(round_up(bytes, 256));
         return o;
     };
-    L->block = block;
     L->z_ld = pitch64(v);
     L->h_ld = pitch64(d);
     L->part_ld = round_up(d, 4);
@@ -227,14 +226,18 @@ size_t ce_total(const muon_linear_ce_t* p, bool grad, int64_t block, CeLayout* L
     L->pack_h = !tma_ready(p->hidden, p->hidden_ld);
     L->w_ld = L->pack_w ? pitch64(d) : p->weight_ld;
     L->sums = grad && block < p->tokens && p->d_weight_dtype != MUON_F32;
+    const int64_t rest = p->tokens % block;
     L->splits = grad ? hidden_splits(block, d, v) : 1;
+    L->last_splits = grad && rest > 0 ? hidden_splits(rest, d, v) : 1;
+    // rows of the larger of the two kinds of blocks' pieces
+    const int64_t pieces = std::max(L->splits > 1 ? L->splits * block : 0, L->last_splits > 1 ? L->last_splits * rest : 0);
     size_t at = kFixedBytes;
     L->w_off = take(at, L->pack_w ? 2 * v * L->w_ld : 0);
     L->sum_off = take(at, L->sums ? 4 * v * d : 0);
     L->tile_off = take(at, 8 * block * train_gemm_max_sums(v));
     L->h_off = take(at, grad || L->pack_h ? 2 * block * L->h_ld : 0);
     L->z_off = take(at, grad ? 4 * block * L->z_ld : 0);
-    L->part_off = take(at, L->splits > 1 ? 4 * L->splits * block * L->part_ld : 0);
+    L->part_off = take(at, 4 * pieces * L->part_ld);
     L->total = at;
     return at;
 }
@@ -246,18 +249,15 @@ bool ce_sizes_ok(const muon_linear_ce_t* p) {
 }
 
 // The largest block of tokens (all of them, or a multiple of 256) that
-// `bytes` holds; 0 when not even 256 fit.
+// `bytes` holds; 0 when not even 256 fit.  A larger block may need less than
+// a smaller one (its d_hidden is cut into fewer pieces), so they are tried one
+// by one, from as many as have room for their logits and sums on.
 int64_t ce_block(const muon_linear_ce_t* p, bool grad, size_t bytes, CeLayout* L) {
     if (ce_total(p, grad, p->tokens, L) <= bytes) return p->tokens;
-    int64_t lo = 0, hi = p->tokens / 256;  // blocks of lo * 256 fit
-    while (lo < hi) {
-        const int64_t mid = (lo + hi + 1) / 2;
-        if (ce_total(p, grad, 256 * mid, L) <= bytes) lo = mid;
-        else hi = mid - 1;
-    }
-    if (lo == 0) return 0;
-    ce_total(p, grad, 256 * lo, L);
-    return 256 * lo;
+    const int64_t row = 8 * train_gemm_max_sums(p->vocab) + (grad ? 4 * pitch64(p->vocab) : 0);
+    for (int64_t n = std::min(p->tokens / 256, static_cast<int64_t>(bytes / 256) / row); n > 0; --n)
+        if (ce_total(p, grad, 256 * n, L) <= bytes) return 256 * n;
+    return 0;
 }
 
 muon_status_t ce_run(const muon_linear_ce_t* p, bool grad, void* workspace, size_t ws_bytes, void* stream) {
@@ -372,8 +372,7 @@ muon_status_t ce_run(const muon_linear_ce_t* p, bool grad, void* workspace, size
         if (e == cudaSuccess) e = grad ? launch_ce_grad_rows(c, st) : launch_ce_finish(c, st);
         if (e != cudaSuccess || !grad) continue;
         // d_hidden = G W; the rows of G lie in the front halves of Z's rows
-        const int splits = m == L.block ? L.splits
-                                        : std::min<int>(hidden_splits(m, d, v), static_cast<int>(L.splits * L.block / m));
+        const int splits = m == block ? L.splits : L.last_splits;
         void* dh = static_cast<uint8_t*>(p->d_hidden) + 2 * t0 * d;
         float* parts = reinterpret_cast<float*>(ws + L.part_off);
         g = TrainGemm{};

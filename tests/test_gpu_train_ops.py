@@ -17,6 +17,7 @@ unit roundoff of a type (2^-24 fp32, 2^-8 bf16, 2^-11 fp16):
     exp(z - lse), a factor of 1 + 2 max|dz| + 2^-18 (the fp32 exponential
     and its argument).
 """
+import ctypes
 import math
 
 import pytest
@@ -307,6 +308,23 @@ def test_cross_entropy_in_blocks_of_tokens(lib, dtype):
     with pytest.raises(m.MuonError) as e:
         m.muon_linear_ce_grad(hidden, weight, targets, workspace=tiny)
     assert e.value.status == 4
+
+
+def test_cross_entropy_short_last_block_stays_in_its_workspace(lib):
+    """Blocks whose d_hidden is summed in one piece, then one in several."""
+    n, v, d = 2048 + 44, 4096, 4864
+    hidden, weight, targets = ce_inputs(13, n, v, d, BF)
+    of = m.train._ce_struct(hidden[:1024], weight, targets[:1024], 1.0, -100)
+    of.d_weight_dtype = 0
+    need = m.load_library().muon_linear_ce_workspace(ctypes.addressof(of), 1, 1 << 40)
+    ws = m.allocate_workspace(need + (8 << 20))
+    ws.fill_(171)
+    dw = torch.empty(v, d, device=DEV)
+    _, _, dh, _ = m.muon_linear_ce_grad(hidden, weight, targets, d_weight=dw, workspace=ws[:need])
+    assert (ws[need:] == 171).all()
+    want = ce_want(hidden, weight, targets, None, 1.0, -100)
+    within(dh, want["dh"], rounded(want["bh"], want["dh"], BF), "d_hidden")
+    within(dw, want["dw"], want["bw"] + 2.0 ** -22 * want["dw"].abs(), "d_weight")
 
 
 @pytest.mark.parametrize("pads", [(0, 0), (3, 5), (8, 16)])

@@ -109,6 +109,32 @@ def test_cross_entropy_workspace(built):
     assert size(ce(dim=0), 1, 1 << 40) == 0
 
 
+@pytest.mark.parametrize("tokens,vocab,dim", [(2000, 32000, 7168), (2048 + 44, 4096, 4864), (5000, 1 << 17, 5120),
+                                              (300, 50021, 13), (4096, 163840, 7168)])
+def test_cross_entropy_takes_the_workspace_it_asked_for(built, tokens, vocab, dim):
+    """Whatever the budget: the size asked for is enough, also when it is the
+    budget."""
+    p = ce(tokens=tokens, vocab=vocab, dim=dim, hidden_ld=dim, weight_ld=dim, targets=1 << 60, loss=1 << 61, lse=1 << 62,
+           weight=1 << 50, d_hidden=1 << 57, d_weight=1 << 58)
+    whole = built.muon_linear_ce_workspace(ctypes.byref(p), 1, 1 << 60)
+    for i in range(41):
+        got = built.muon_linear_ce_workspace(ctypes.byref(p), 1, whole * i // 40)
+        assert built.muon_linear_ce_workspace(ctypes.byref(p), 1, got) <= got
+        assert built.muon_linear_ce_grad(ctypes.byref(p), P(1 << 40), got, None) != SMALL
+
+
+def test_cross_entropy_workspace_of_a_short_last_block(built):
+    """1024 tokens' d_hidden (4 x 19 tiles, one per pair of CTAs) is summed in
+    one piece, 44 tokens' in at least two, which take room of their own: what
+    holds 2048 tokens in two such blocks does not hold 44 more in a third."""
+    of = dict(vocab=4096, dim=4864, hidden_ld=4864, weight_ld=4864, d_weight_dtype=0)
+    size = lambda n, budget: built.muon_linear_ce_workspace(ctypes.byref(ce(tokens=n, **of)), 1, budget)  # noqa: E731
+    block = size(1024, 1 << 40)
+    assert size(2048, block) == block
+    more = next(extra for extra in range(0, 16 << 20, 256) if size(2048 + 44, block + extra) >= block)
+    assert more >= 2 * 4 * 44 * 4864
+
+
 def mm(lib, x=4096, xld=64, w=1 << 20, off=1 << 22, odt=0, dt=1, e=3, n=10, r=32, c=64, tr=0, y=1 << 23, yld=32,
        ws=1 << 24, wsb=1 << 20):
     return lib.muon_expert_matmul(P(x), xld, P(w), P(off), odt, dt, e, n, r, c, tr, P(y), yld, P(ws), wsb, None)
