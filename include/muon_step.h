@@ -426,9 +426,10 @@ muon_status_t muon_linear_ce(const muon_linear_ce_t* p, void* workspace, size_t 
 /* loss, lse and both gradients of sum_t row_scale[t] * loss[t]:
  *   g[t][v]  = row_scale[t] (exp(z - lse) - [v == targets[t]]), 0 when ignored
  *   d_hidden = logit_scale g weight;  d_weight = logit_scale g^T hidden
- * g is rounded once to `dtype`, relative to the largest |row_scale|; the sums
- * are fp32.  Ignored tokens' hidden rows do not enter d_weight, whatever
- * they hold. */
+ * g is rounded once to `dtype`, relative to the largest |row_scale| of the
+ * tokens that count (one that is not finite makes every gradient so); the sums
+ * are fp32.  Ignored tokens' hidden rows and row_scale enter no other token's
+ * results, whatever they hold. */
 muon_status_t muon_linear_ce_grad(const muon_linear_ce_t* p, void* workspace, size_t ws_bytes,
                                   void* stream);
 

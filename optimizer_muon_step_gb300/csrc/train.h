@@ -83,7 +83,8 @@ struct CeEpilogue {
     float scale2;            // log2(e) * logit_scale
     const float* row_scale;  // the call's, may be null
     int64_t tokens;          // of the call
-    float* scalars;          // [0] the largest |row_scale| (1 when null), [1] that times factor
+    int64_t ignore_index;
+    float* scalars;          // [0] the largest |row_scale| of the tokens that count (1 when null), [1] that times factor
     float factor;
 };
 

@@ -365,6 +365,7 @@ muon_status_t ce_run(const muon_linear_ce_t* p, bool grad, void* workspace, size
         g.ce.scale2 = p->logit_scale * 1.4426950408889634f;
         g.ce.row_scale = grad ? p->row_scale : nullptr;
         g.ce.tokens = n;
+        g.ce.ignore_index = p->ignore_index;
         g.ce.scalars = scalars;
         g.ce.factor = p->logit_scale / ce_grad_lift(p->dtype);
         g.kind = MUON_KERNEL_CE_LOGITS;

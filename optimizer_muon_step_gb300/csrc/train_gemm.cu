@@ -342,13 +342,15 @@ struct RowSums {
 };
 
 // The scalars of a loss call, by one warp while the first tile's products
-// are under way.
-__device__ __forceinline__ void write_scalars(const CeEpilogue& ce, int lane) {
+// are under way.  Ignored tokens' scales do not count, whatever they hold.
+__device__ __forceinline__ void write_scalars(const CeEpilogue& ce, int64_t vocab, int lane) {
     float m = ce.row_scale ? 0.f : 1.f;
     if (ce.row_scale) {
 #pragma unroll 8
         for (int64_t t = lane; t < ce.tokens; t += 32) {
-            const float a = fabsf(ce.row_scale[t]);
+            const int64_t target = load_index(ce.targets, ce.targets64, t);
+            const bool counts = target >= 0 && target < vocab && target != ce.ignore_index;
+            const float a = counts ? fabsf(ce.row_scale[t]) : 0.f;
             m = isnan(a) || a > m ? a : m;
         }
     }
@@ -594,7 +596,7 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
         wait_drain(smem_u32(drain_bar), 0);
     } else if (warp == 1) {
         // the odd CTA's second warp has no part in the product
-        if (kCe && kPair && p.ce.first && blockIdx.x == 1) write_scalars(p.ce, lane);
+        if (kCe && kPair && p.ce.first && blockIdx.x == 1) write_scalars(p.ce, p.N, lane);
     } else {
         // ---------------- epilogue ----------------
         const int quarter = warp & 3;       // TMEM lanes 32 * quarter .. + 31
@@ -602,7 +604,7 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
         uint8_t* buf = ebufs + (warp - 2) * EBUF_BYTES;  // a block on its way to C
         int local = 0;
         const float alpha = p.alpha_dev ? p.alpha * *p.alpha_dev : p.alpha;
-        if (kCe && !kPair && p.ce.first && blockIdx.x == 0 && warp == 2) write_scalars(p.ce, lane);
+        if (kCe && !kPair && p.ce.first && blockIdx.x == 0 && warp == 2) write_scalars(p.ce, p.N, lane);
         bool ok = true;
         for (int i = 0; ok && read_tile(i, tile); ++i) {
             const int row = tile.row0 + rank * BM + quarter * 32;

@@ -351,6 +351,19 @@ def test_cross_entropy_ignored_rows_are_not_read_into_the_gradients(lib):
     assert (dh[::3] == 0).all() and (loss[::3] == 0).all()
 
 
+@pytest.mark.parametrize("held", [float("nan"), float("inf"), -1e30])
+@pytest.mark.parametrize("n", [90, 300])
+def test_cross_entropy_ignored_rows_scale_is_not_read(lib, n, held):
+    hidden, weight, targets = ce_inputs(n, n, 500, 72, HF, ignored=0.2)
+    targets[1], targets[2] = 500, -7                     # outside: left out as well
+    out = (targets < 0) | (targets >= 500)
+    scale = torch.rand(n, generator=gen(n), device=DEV) / n
+    want = m.muon_linear_ce_grad(hidden, weight, targets, row_scale=torch.where(out, 0.0, scale))
+    got = m.muon_linear_ce_grad(hidden, weight, targets, row_scale=torch.where(out, held, scale))
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
 def test_cross_entropy_all_ignored_and_targets_outside(lib):
     hidden, weight, targets = ce_inputs(41, 70, 300, 64, BF)
     need = m.muon_linear_ce_workspace(hidden, weight, targets, True)
