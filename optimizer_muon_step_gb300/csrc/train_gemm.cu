@@ -326,10 +326,11 @@ struct RowSums {
         for (int k = 3; k < 32; ++k) m[k & 3] = fmaxf(m[k & 3], v[k]);
         const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
         // an infinite maximum is not subtracted: inf - inf would be NaN where
-        // the sum is inf, and -inf leaves the sum at 0
+        // the sum is inf, and -inf leaves the sum at 0 (or NaN, where all
+        // columns so far were: a maximum passes NaN over)
         const float ref = isinf(most) ? 0.f : most;
         const uint64_t r2 = pack2(-ref, -ref);
-        uint64_t part[2] = {pack2(top == -INFINITY ? 0.f : sum * ex2((isinf(top) ? 0.f : top) - ref), 0.f), pack2(0.f, 0.f)};
+        uint64_t part[2] = {pack2(top == -INFINITY ? sum : sum * ex2((isinf(top) ? 0.f : top) - ref), 0.f), pack2(0.f, 0.f)};
 #pragma unroll
         for (int k = 0; k < 32; k += 2) {
             const float2 x = unpack2(add2(pack2(v[k], v[k + 1]), r2));

@@ -351,6 +351,19 @@ def test_cross_entropy_ignored_rows_are_not_read_into_the_gradients(lib):
     assert (dh[::3] == 0).all() and (loss[::3] == 0).all()
 
 
+@pytest.mark.parametrize("d", [64, 1032])
+@pytest.mark.parametrize("lo,hi", [(0, 32), (128, 160), (64, 128), (576, 600), (31, 33)])
+def test_cross_entropy_nan_columns_reach_the_loss(lib, d, lo, hi):
+    """NaN logits of some columns, whole blocks of them among these, are not
+    lost on the way to the normaliser."""
+    for n in (20, 150):
+        hidden, weight, targets = ce_inputs(n, n, 600, d, BF)
+        targets[:] = 300
+        weight[lo:hi] = float("nan")
+        loss, lse = m.muon_linear_ce(hidden, weight, targets)
+        assert torch.isnan(loss).all() and torch.isnan(lse).all()
+
+
 @pytest.mark.parametrize("held", [float("nan"), float("inf"), -1e30])
 @pytest.mark.parametrize("n", [90, 300])
 def test_cross_entropy_ignored_rows_scale_is_not_read(lib, n, held):
