@@ -281,6 +281,19 @@ def test_expert_wgrad_long_sums(lib):
         expert_check(x, dy, w, off, BF)
 
 
+def test_expert_wgrad_one_long_sum_of_many(lib):
+    """One expert has all of 20000 tokens: its fp32 sums of positive products
+    are cut too.  A segment's 1024 terms are 64 tensor-core additions, off by
+    at most 2^-23 of the sum each, and the 20 segments are added in fp32."""
+    off = torch.tensor([0] * 18 + [20000] * 23, dtype=torch.int32, device=DEV)
+    g = gen(5)
+    x, dy = (torch.rand(20000, c, generator=g, device=DEV).to(BF) for c in (200, 136))
+    got = m.muon_expert_wgrad(dy, x, off, out_dtype=F32)
+    want = dy.double().t() @ x.double()
+    assert (got[:17] == 0).all() and (got[18:] == 0).all()
+    assert ((got[17].double() - want).abs() <= (64 * 2.0 ** -23 + 20 * 2.0 ** -24) * want).all()
+
+
 @pytest.mark.parametrize("dtype", [BF, HF])
 def test_cross_entropy_in_blocks_of_tokens(lib, dtype):
     """A workspace that holds 256 tokens: the gradient of the weights is summed
