@@ -121,18 +121,33 @@ struct Walker {
     // and after all groups.  One window, so one round trip to memory, for up
     // to 254 groups.
     static constexpr int kPer = 8;
+    static constexpr int kUnit = TILE_M == BM ? 16 : 32;  // tokens the MMA's N goes by
+    // Pairs take the groups of a window by falling width of their tiles, which
+    // are then dealt out to and fro, so that the workers end together: with the
+    // even widths below, 16 experts of 900 to 2400 tokens, 2048 x 2048, take
+    // 132 us for 140, 64 of 0 to 2077 tokens 135 for 139, equal ones the same.
+    // Single CTAs have a few tiles each and wait for memory: their order does
+    // not matter.
+    static constexpr bool kSorted = TILE_M != BM;
     int base, first, total, incl;
-    int edge[kPer + 1];  // the lane's group i has tokens [edge[i], edge[i + 1])
+    int edge[kPer + 1];    // the lane's group i has tokens [edge[i], edge[i + 1])
+    uint32_t widths;       // kSorted: 4 bits for each, the units of its widest tile
+    uint32_t todo, width;  // kSorted: the widths that are still to come, and the one at hand
 
-    __device__ Walker(const GemmParams& prm, int ln) : p(prm), lane(ln), base(-1 - 32 * kPer), first(0), total(0), incl(0) {}
+    __device__ Walker(const GemmParams& prm, int ln)
+        : p(prm), lane(ln), base(-1 - 32 * kPer), first(0), total(0), incl(0), widths(0), todo(0), width(0) {}
 
     // where group e begins (groups + 1: where the tokens after all groups end)
     __device__ int begin_of(int e) const { return e < 0 ? 0 : e > p.groups ? p.N : clamped(p, e, p.N); }
 
     __device__ int tiles_of(int i) const {
         const int n = edge[i + 1] - edge[i];
-        return n > 0 ? (n + p.bn - 1) / p.bn * p.tiles_m : 0;
+        const bool now = !kSorted || ((widths >> (4 * i)) & 15) == width;
+        return n > 0 && now ? tiles_across(n) * p.tiles_m : 0;
     }
+
+    // tiles of n tokens; pairs always work on tiles of up to BN
+    __device__ int tiles_across(int n) const { return kSorted ? (n + BN - 1) / BN : (n + p.bn - 1) / p.bn; }
 
     __device__ bool next(int t, Tile& o) {
         if (p.group != GROUP_M) {
@@ -173,10 +188,32 @@ struct Walker {
         }
         while (t >= first + total) {
             first += total;
-            base += 32 * kPer;
-            if (base > p.groups) return false;
+            if (todo == 0) {
+                base += 32 * kPer;
+                if (base > p.groups) return false;
 #pragma unroll
-            for (int i = 0; i <= kPer; ++i) edge[i] = begin_of(base + lane * kPer + i);
+                for (int i = 0; i <= kPer; ++i) edge[i] = begin_of(base + lane * kPer + i);
+                todo = 1;
+                if (kSorted) {
+                    todo = widths = 0;
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i) {
+                        const int n = edge[i + 1] - edge[i];
+                        if (n <= 0) continue;
+                        const int tn = tiles_across(n), units = (n + kUnit - 1) / kUnit;
+                        int w = 1;  // units / tn, rounded up
+#pragma unroll
+                        for (int k = 1; k < BN / kUnit; ++k) w += k * tn < units;
+                        widths |= static_cast<uint32_t>(w) << (4 * i);
+                        todo |= 1u << w;
+                    }
+                    todo = __reduce_or_sync(0xffffffffu, todo);
+                }
+            }
+            total = 0;
+            if (todo == 0) continue;
+            width = 31 - __clz(static_cast<int>(todo));
+            todo &= ~(1u << width);
             incl = 0;
 #pragma unroll
             for (int i = 0; i < kPer; ++i) incl += tiles_of(i);
@@ -210,16 +247,18 @@ struct Walker {
         a = __shfl_sync(0xffffffffu, a, src);
         e = __shfl_sync(0xffffffffu, e, src);
         at = __shfl_sync(0xffffffffu, at, src);
-        const int tn = (e - a + p.bn - 1) / p.bn;
+        const int tn = tiles_across(e - a);
         const int m = r / tn;
         const int g = base + src * kPer + at;
-        // the group's tokens in tn tiles of equal width
-        constexpr int q = TILE_M == BM ? 15 : 31;
-        const int w = ((e - a + tn - 1) / tn + q) & ~q;
+        // the group's tokens in tn tiles as even as whole units allow, which
+        // pads a group by less than a unit, not every tile
+        const int units = (e - a + kUnit - 1) / kUnit, j = r - m * tn;
+        const int per = units / tn, more = units - per * tn;
+        const int w = kUnit * (per + (j < more ? 1 : 0));
         o.row0 = m * TILE_M;
         o.rows_end = p.M;
         o.tn = 0;
-        o.col0 = a + (r - m * tn) * w;
+        o.col0 = a + kUnit * (j * per + (j < more ? j : more));
         o.cols_end = o.col0 + w < e ? o.col0 + w : e;
         o.n = w;
         o.c2 = 0;
@@ -459,7 +498,7 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
             // groups of falling size are dealt out to and fro: the workers' sums
             // of k-blocks end within 2% of each other where one direction leaves
             // 4%, and groups in their given order 8 to 16%
-            const bool back = p.group == GROUP_K && (i & 1);
+            const bool back = (p.group == GROUP_K || (p.group == GROUP_M && kPair)) && (i & 1);
             const bool more = walk.next(i * workers + (back ? workers - 1 - worker : worker), tile);
             const int s = i % TILE_SLOTS;
             if (!wait_bounded(smem_u32(&sempty_bar[s]), (static_cast<uint32_t>(i / TILE_SLOTS) & 1u) ^ 1u, abort_flag,
