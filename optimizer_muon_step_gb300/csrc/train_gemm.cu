@@ -35,6 +35,16 @@
 // The softmax epilogue (CE) reduces each row of a logits tile to its maximum
 // and sum of exponentials straight from TMEM; the logits are stored only
 // when their gradient is wanted.
+//
+// What bounds it, bf16, on a card that holds 1.3 to 1.5 GHz under this load:
+//   16 rows x 163840 columns, K 2048     reading the 671 MB of B: 109 us
+//   4096 x 50021, K 2048, CE             tensor pipe: 420 us, 2.0 PFLOP/s
+//   4096 x 163840, K 7168, three products of a gradient   tensor pipe at the
+//                                        power limit: 1.6 to 1.7 PFLOP/s
+//   GROUP_M, 64 experts x 512 tokens, 2048 x 2048   169 us, 1.63 PFLOP/s
+//   GROUP_K, the same                    190 us, 1.44 PFLOP/s: 8 k-blocks a
+//                                        tile, then its 128 KB; without the
+//                                        stores it takes 154 us
 #include <string.h>
 
 #include "host_checks.h"
@@ -62,7 +72,8 @@ constexpr int MAX_STAGES = 12;
 constexpr int SMEM_BYTES = 1024 + RING_BYTES + EBUFS_BYTES + 1024;
 
 // What a product's tiles end in.
-// The LONG ones cut the sum over K into segments (see the epilogue).
+// The LONG ones cut the sum over K into segments (see the epilogue); they
+// take 1 to 3% longer in the loss, 4 to 10% in GROUP_K's short sums.
 // Terms summed by the tensor core in one go: 1024 where 32 bits of the sum
 // count (2e-6 off at 2048, 9e-6 at 8192), 16384 (2e-5) where the result is
 // rounded to 16 bits.
@@ -955,7 +966,8 @@ __global__ void pack_kernel(const uint16_t* src, int64_t src_ld, uint16_t* dst, 
 }
 
 // out = alpha * sum over the splits, in order; four columns a thread (rows
-// are padded to four).
+// are padded to four).  The pieces come out of L2: 8 us for 999 x 1000 in 8
+// pieces, most of it the launch and the loads' latency.
 template <int DT>
 __global__ void __launch_bounds__(256) split_sum_kernel(const float* parts, int64_t ld, int64_t stride, int splits,
                                                         float alpha, const float* alpha_dev, void* out, int64_t out_ld,
@@ -1083,6 +1095,10 @@ cudaError_t setup(int* max_pairs) {
 }
 
 // Pairs halve each SM's operand traffic but work on 256 rows at a time.
+// GROUP_M, 64 experts, 2048 -> 1408, single CTAs and pairs: 96 tokens an
+// expert 75 and 75 us, 128 tokens 85 and 75, 384 tokens 129 and 115.  With
+// fewer tokens the singles' narrow tiles win (16 tokens: 62 us with 64
+// columns, 69 with 256).
 bool use_pairs(const TrainGemm& g) {
     if (g.group == GROUP_M) return g.M > BM && g.N >= g.groups * 128;
     return g.M > BM;
@@ -1154,7 +1170,10 @@ cudaError_t train_gemm(const TrainGemm& g, int num_sms, cudaStream_t st) {
     if (g.ce.sums) {
         bn = train_gemm_bn(g.M, g.N, g.K);
     } else if (end == END_TOKENS) {
-        // about the tokens of two average experts, so that few experts need two tiles
+        // about the tokens of two average experts, so that few experts need two
+        // tiles, and more of the ring is weights (64 experts, 2048 -> 1408, one
+        // token each: 38 us with 64 columns, 42 with 256; 16 each: 62 with
+        // 64, 69 with 256)
         const int64_t want = 2 * ((g.N + g.groups - 1) / g.groups);
         bn = pair || want > 128 ? 256 : want > 64 ? 128 : want > 32 ? 64 : 32;
     }
@@ -1224,9 +1243,13 @@ cudaError_t train_gemm(const TrainGemm& g, int num_sms, cudaStream_t st) {
     }
     if (tiles > INT32_MAX) return cudaErrorInvalidValue;
     p.total_tiles = static_cast<int32_t>(tiles);
-    // all rows of tiles together while the A operand stays in L2 (so that B
-    // is read once), else bands of 8 that share both operands' tiles
-    p.band = g.M * g.K * 2 <= (int64_t(48) << 20) ? p.tiles_m : 8;
+    // All rows of tiles together where A stays in L2 and B does not, which is
+    // then read once (4096 x 50021, K 2048: 419 us, in bands of 8 429); else
+    // bands of 8 that share both operands' tiles and write whole rows of C soon
+    // after each other (a gradient's last two products, 16 x 163840, K 2048:
+    // 224 us, together 245; 4096 x 50021, K 7168: 3.4 ms, together 3.8).
+    const int64_t l2 = int64_t(48) << 20;
+    p.band = g.M * g.K * 2 <= l2 && g.N * g.K * 2 > l2 ? p.tiles_m : 8;
     if (g.group == GROUP_K) {
         GroupMapParams m;
         memset(&m, 0, sizeof m);
