@@ -26,13 +26,16 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
+// The sum of a (top, sum) pair relative to another maximum.
+__device__ __forceinline__ float rescaled(float2 a, float ref) {
+    return a.x == -INFINITY ? a.y : a.y * exp2_fast((isinf(a.x) ? 0.f : a.x) - ref);
+}
+
 // (top, sum) pairs of disjoint column sets; an infinite top is not subtracted.
 __device__ __forceinline__ float2 join(float2 a, float2 b) {
     const float m = fmaxf(a.x, b.x);
     const float ref = isinf(m) ? 0.f : m;
-    const float sa = a.x == -INFINITY ? a.y : a.y * exp2_fast((isinf(a.x) ? 0.f : a.x) - ref);
-    const float sb = b.x == -INFINITY ? b.y : b.y * exp2_fast((isinf(b.x) ? 0.f : b.x) - ref);
-    return make_float2(m, sa + sb);
+    return make_float2(m, rescaled(a, ref) + rescaled(b, ref));
 }
 
 // What one CTA finds out about a row: the target's logit, and the normaliser
@@ -52,13 +55,14 @@ __device__ __forceinline__ bool wide_rows(const CeBlock& b) {
 template <int DT, int kThreads>
 __device__ __forceinline__ Row find_row(const CeBlock& b, int64_t t) {
     typedef typename Elem<DT>::T T;
-    __shared__ float2 part[kThreads / 32];
-    __shared__ float dot[kThreads / 32];
+    constexpr int kWarps = kThreads / 32;
+    __shared__ float tops[kWarps], sums[kWarps], dots[kWarps];
     Row r;
     r.target = load_index(b.targets, b.targets64, t);
     r.inside = r.target >= 0 && r.target < b.vocab;
     r.live = r.inside && r.target != b.ignore_index;
     float2 acc = make_float2(-INFINITY, 0.f);
+#pragma unroll 4
     for (int64_t i = threadIdx.x; i < b.row_sums; i += kThreads) acc = join(acc, b.sums[t * b.row_sums + i]);
     float s = 0.f;
     if (r.inside) {
@@ -76,22 +80,34 @@ __device__ __forceinline__ Row find_row(const CeBlock& b, int64_t t) {
             for (int64_t c = threadIdx.x; c < b.dim; c += kThreads) s = fmaf(Elem<DT>::load(h[c]), Elem<DT>::load(w[c]), s);
         }
     }
+    // the row's maximum first, then one exponential a thread
+    float top = acc.x;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-        acc = join(acc, make_float2(__shfl_xor_sync(0xffffffffu, acc.x, o), __shfl_xor_sync(0xffffffffu, acc.y, o)));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         s += __shfl_xor_sync(0xffffffffu, s, o);
     }
     if ((threadIdx.x & 31) == 0) {
-        part[threadIdx.x >> 5] = acc;
-        dot[threadIdx.x >> 5] = s;
+        tops[threadIdx.x >> 5] = top;
+        dots[threadIdx.x >> 5] = s;
     }
     __syncthreads();
-    acc = part[0];
-    s = dot[0];
-    for (int i = 1; i < kThreads / 32; ++i) {
-        acc = join(acc, part[i]);
-        s += dot[i];
+    top = tops[0];
+    s = dots[0];
+#pragma unroll
+    for (int i = 1; i < kWarps; ++i) {
+        top = fmaxf(top, tops[i]);
+        s += dots[i];
     }
+    float sum = rescaled(acc, isinf(top) ? 0.f : top);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    sum = sums[0];
+#pragma unroll
+    for (int i = 1; i < kWarps; ++i) sum += sums[i];
+    acc = make_float2(top, sum);
     r.zt = b.logit_scale * s;
     if (r.inside) acc = join(acc, make_float2(r.zt * kLog2e, isnan(r.zt) ? r.zt : 1.f));
     r.lse2 = (isinf(acc.x) ? 0.f : acc.x) + log2f(acc.y);
@@ -106,14 +122,27 @@ __device__ __forceinline__ void put_loss(const CeBlock& b, int64_t t, const Row&
 }
 
 // Loss and normaliser alone; one CTA per token, which reads the token's tile
-// sums (1280 pairs at 163840 columns of 256) and two rows for the target's
-// logit: a few microseconds of latency after products of 100 us and more.
-constexpr int kFinishThreads = 128;
-template <int DT>
-__global__ void __launch_bounds__(kFinishThreads) ce_finish_kernel(const __grid_constant__ CeBlock b) {
+// sums (2560 pairs at 163840 columns of 128) and two rows for the target's
+// logit: microseconds of latency after products of 100 us and more.  512
+// threads have the most loads in flight, as long as all CTAs fit at once; many
+// tokens are bound by the instructions that a CTA needs anyhow.  The whole
+// loss with 512 and 128 threads: 16 x 163840, K 2048, 106 and 111 us; 300 x
+// 50021, K 512, 25 and 26.5; 2048 x 50021, K 2048, 224 and 217; 8192 x 32000,
+// K 512, 177 and 153.
+constexpr int kFewThreads = 512, kManyThreads = 128;
+constexpr int kFewTokens = 152 * (2048 / kFewThreads);
+template <int DT, int kThreads>
+__global__ void __launch_bounds__(kThreads) ce_finish_kernel(const __grid_constant__ CeBlock b) {
     pdl_wait_then_release();
-    const Row r = find_row<DT, kFinishThreads>(b, blockIdx.x);
+    const Row r = find_row<DT, kThreads>(b, blockIdx.x);
     if (threadIdx.x == 0) put_loss(b, blockIdx.x, r);
+}
+
+template <int DT>
+cudaError_t finish_go(const CeBlock& b, cudaStream_t st) {
+    const dim3 grid(static_cast<unsigned>(b.tokens));
+    if (b.tokens <= kFewTokens) return launch_pdl(ce_finish_kernel<DT, kFewThreads>, grid, dim3(kFewThreads), 0, st, b);
+    return launch_pdl(ce_finish_kernel<DT, kManyThreads>, grid, dim3(kManyThreads), 0, st, b);
 }
 
 constexpr int kRowThreads = 512;
@@ -191,8 +220,7 @@ __global__ void round_kernel(const float* src, typename Elem<DT>::T* dst, int64_
 
 cudaError_t launch_ce_finish(const CeBlock& b, cudaStream_t st) {
     launch_begin(MUON_KERNEL_CE_ROWS, st);
-    const cudaError_t e = launch_pdl(b.dtype == MUON_BF16 ? ce_finish_kernel<MUON_BF16> : ce_finish_kernel<MUON_F16>,
-                                     dim3(static_cast<unsigned>(b.tokens)), dim3(kFinishThreads), 0, st, b);
+    const cudaError_t e = b.dtype == MUON_BF16 ? finish_go<MUON_BF16>(b, st) : finish_go<MUON_F16>(b, st);
     launch_end(MUON_KERNEL_CE_ROWS, st);
     return e;
 }

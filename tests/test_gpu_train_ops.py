@@ -253,6 +253,15 @@ def test_cross_entropy_and_gradients(lib, dtype, n, v, d):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_cross_entropy_loss_of_many_tokens(lib, dtype):
+    hidden, weight, targets = ce_inputs(23, 2100, 700, 40, dtype, ignored=0.2)
+    want = ce_want(hidden, weight, targets, None, 1.0, -100)
+    loss, lse = m.muon_linear_ce(hidden, weight, targets)
+    within(loss, want["loss"], want["loss_bound"], "loss")
+    within(lse, want["lse"], want["lse_bound"], "lse")
+
+
 @pytest.mark.parametrize("n,v,d", [(100, 900, 1400), (200, 1500, 2056), (1100, 100, 72), (1100, 400, 72), (1800, 20000, 2048),
                                    (128, 100000, 7168)])
 def test_cross_entropy_long_sums(lib, n, v, d):
