@@ -360,7 +360,7 @@ struct SumArgs {
     float* parts;          // [2 * piece + slot][part_ld]: slot 0 a run that began before, 1 one that goes on
     float* d_table;
     int64_t grad_ld, part_ld, dim;
-    int32_t piece, pieces, col_tasks, accumulate;
+    int32_t tokens, piece, pieces, col_tasks, accumulate;
     float scale;
 };
 
@@ -400,12 +400,16 @@ __device__ __forceinline__ void sum_piece(const SumArgs& a, int piece, int64_t c
     typedef typename Elem<GD>::T TG;
     const TG* grad = static_cast<const TG*>(a.grad);
     const int i0 = piece * a.piece;
-    const int n = min(*a.live - i0, a.piece);
-    if (n <= 0) return;
-    const int key = lane < n ? a.keys[i0 + lane] : -1;
-    const int pos = lane < n ? a.pos[i0 + lane] : 0;
+    // loaded together; positions from `live` on hold nothing
+    const int live = *a.live;
+    const bool here = lane < a.piece && i0 + lane < a.tokens;
+    const int held_key = here ? a.keys[i0 + lane] : 0, held_pos = here ? a.pos[i0 + lane] : 0;
     const int prev = i0 > 0 ? a.keys[i0 - 1] : -1;
-    const int next = i0 + n < *a.live ? a.keys[i0 + n] : -1;
+    const int held_next = i0 + a.piece < a.tokens ? a.keys[i0 + a.piece] : 0;
+    const int n = min(live - i0, a.piece);
+    if (n <= 0) return;
+    const int key = lane < n ? held_key : -1, pos = lane < n ? held_pos : 0;
+    const int next = i0 + a.piece < live ? held_next : -1;
     float acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.f;
@@ -477,19 +481,26 @@ __global__ void __launch_bounds__(32 * kSumWarps, kWide ? 6 : 4) embed_sum_kerne
         sum_piece<GD, kWide>(a, static_cast<int>(piece), (task - piece * a.col_tasks) * kCols, threadIdx.x & 31);
 }
 
-// First sorted position whose key is not below v, by a warp: 32 probes a step.
-__device__ __forceinline__ int lower_bound(const int32_t* keys, int n, int64_t v, int lane) {
+// First sorted position of key v and the one after its last, by a warp: half
+// of it searches for either, 16 probes a step.
+__device__ __forceinline__ int2 find_run(const int32_t* keys, int n, int v, int lane) {
+    const int half = lane >> 4, l = lane & 15;
     int lo = 0, hi = n;  // in [lo, hi]
-    while (hi > lo) {
-        const int step = (hi - lo + 31) / 32;
-        const int at = lo + lane * step;
-        const int below = __popc(__ballot_sync(0xffffffffu, at < hi && keys[at < hi ? at : lo] < v));
-        if (below == 0) return lo;
-        const int next = lo + below * step;  // the first probe that is not below
-        lo = lo + (below - 1) * step + 1;
-        hi = next < hi ? next : hi;
+    while (__any_sync(0xffffffffu, hi > lo)) {
+        const int step = (hi - lo + 15) / 16;
+        const int at = lo + l * step;
+        bool below = false;
+        if (at < hi) below = half ? keys[at] <= v : keys[at] < v;
+        const int count = __popc((__ballot_sync(0xffffffffu, below) >> (16 * half)) & 0xffff);
+        if (count == 0) {
+            hi = lo;
+        } else {
+            const int next = lo + count * step;  // the first probe that is not below
+            lo += (count - 1) * step + 1;
+            hi = next < hi ? next : hi;
+        }
     }
-    return lo;
+    return make_int2(__shfl_sync(0xffffffffu, lo, 0), __shfl_sync(0xffffffffu, lo, 16));
 }
 
 // The runs that cross pieces.  One of up to 32 pieces is added by the CTA of
@@ -519,15 +530,17 @@ __global__ void __launch_bounds__(256) embed_join_kernel(const __grid_constant__
     pdl_wait_then_release();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int piece = blockIdx.x, end = (piece + 1) * a.piece;
-    const int live = *a.live;
-    if (end >= live) return;
-    const int key = a.keys[end - 1];
     // pieces of the run after this one (those whose first key is its key) and
-    // before it (last key), up to 32 each
+    // before it (last key), up to 32 each; all loaded together, which is most of
+    // this kernel's time where few runs cross
     const int64_t f = (piece + 1 + lane) * static_cast<int64_t>(a.piece), b = (piece - lane) * static_cast<int64_t>(a.piece) - 1;
-    const int after = __popc(__ballot_sync(0xffffffffu, f < live && a.keys[f < live ? f : 0] == key));
-    const bool whole = a.keys[end - a.piece] == key;  // the run fills this piece
-    const int before = __popc(__ballot_sync(0xffffffffu, whole && b >= 0 && a.keys[b >= 0 ? b : 0] == key));
+    const int live = *a.live;
+    const int key = a.keys[end - 1], begin_key = a.keys[end - a.piece];
+    const int f_key = f < a.tokens ? a.keys[f] : 0, b_key = b >= 0 ? a.keys[b] : 0;
+    if (end >= live) return;
+    const int after = __popc(__ballot_sync(0xffffffffu, f < live && f_key == key));
+    const bool whole = begin_key == key;  // the run fills this piece
+    const int before = __popc(__ballot_sync(0xffffffffu, whole && b >= 0 && b_key == key));
     if (after == 0) return;
     float* row = a.d_table + static_cast<int64_t>(key) * a.dim;
     if (before + after < 32) {
@@ -540,8 +553,8 @@ __global__ void __launch_bounds__(256) embed_join_kernel(const __grid_constant__
         return;
     }
     if (blockIdx.y != 0) return;
-    const int first = lower_bound(a.keys, live, key, lane) / a.piece;
-    const int last = (lower_bound(a.keys, live, static_cast<int64_t>(key) + 1, lane) - 1) / a.piece;
+    const int2 run = find_run(a.keys, live, key, lane);
+    const int first = run.x / a.piece, last = (run.y - 1) / a.piece;
     const int count = last - first + 1, per = (count + 7) / 8;
     const int lo = warp * per, hi = min(lo + per, count);
     // the run's pieces but its last one have a CTA each
@@ -676,6 +689,7 @@ cudaError_t launch_embed_grad(const EmbedGrad& a, void* workspace, int num_sms, 
     m.part_ld = L.part_ld;
     m.dim = a.dim;
     m.col_tasks = static_cast<int32_t>((a.dim + kCols - 1) / kCols);
+    m.tokens = static_cast<int32_t>(a.tokens);
     m.piece = sum_piece_size(a.tokens, a.dim);
     m.pieces = static_cast<int32_t>((a.tokens + m.piece - 1) / m.piece);
     m.accumulate = a.accumulate;
