@@ -114,6 +114,29 @@ __device__ __forceinline__ Row find_row(const CeBlock& b, int64_t t) {
     return r;
 }
 
+// Of the row's gradient, see ce_grad_lift and CeEpilogue::scalars.
+template <int DT>
+__device__ __forceinline__ float grad_scale(const CeBlock& b, int64_t t) {
+    const float top = b.scalars[0];
+    return ce_grad_lift(DT) * (b.row_scale ? (top > 0.f ? b.row_scale[t] / top : 0.f) : 1.f);
+}
+
+__device__ __forceinline__ float hot_of(const Row& r) { return exp2_fast(r.zt * kLog2e - r.lse2) - 1.f; }
+
+// The hidden row for d_weight's product, zeros when ignored.
+template <int DT, int kThreads>
+__device__ __forceinline__ void copy_hidden(const CeBlock& b, int64_t t, bool live) {
+    typedef typename Elem<DT>::T T;
+    const T* h = static_cast<const T*>(b.hidden) + t * b.hidden_ld;
+    T* copy = static_cast<T*>(b.packed) + t * b.packed_ld;
+    if (wide_rows(b)) {
+        for (int64_t c = 8 * threadIdx.x; c < b.dim; c += 8 * kThreads)
+            *reinterpret_cast<uint4*>(copy + c) = live ? *reinterpret_cast<const uint4*>(h + c) : make_uint4(0u, 0u, 0u, 0u);
+    } else {
+        for (int64_t c = threadIdx.x; c < b.dim; c += kThreads) copy[c] = live ? h[c] : Elem<DT>::store(0.f);
+    }
+}
+
 __device__ __forceinline__ void put_loss(const CeBlock& b, int64_t t, const Row& r) {
     const float lse = r.lse2 * kLn2;
     b.lse[t] = lse;
@@ -134,8 +157,19 @@ constexpr int kFewTokens = 152 * (2048 / kFewThreads);
 template <int DT, int kThreads>
 __global__ void __launch_bounds__(kThreads) ce_finish_kernel(const __grid_constant__ CeBlock b) {
     pdl_wait_then_release();
-    const Row r = find_row<DT, kThreads>(b, blockIdx.x);
-    if (threadIdx.x == 0) put_loss(b, blockIdx.x, r);
+    const int64_t t = blockIdx.x;
+    const Row r = find_row<DT, kThreads>(b, t);
+    if (threadIdx.x == 0) put_loss(b, t, r);
+    if (!b.rows) return;
+    copy_hidden<DT, kThreads>(b, t, r.live);
+    if (threadIdx.x == 0) {
+        CeRow o;
+        o.lse2 = r.lse2;
+        o.scale = grad_scale<DT>(b, t);
+        o.hot = hot_of(r);
+        o.target = r.live ? static_cast<int32_t>(r.target) : -1;
+        b.rows[t] = o;
+    }
 }
 
 template <int DT>
@@ -148,7 +182,7 @@ cudaError_t finish_go(const CeBlock& b, cudaStream_t st) {
 constexpr int kRowThreads = 512;
 constexpr int kRowStep = 8 * kRowThreads;  // logits of one sweep
 
-// Loss, normaliser and the logits' gradient in place, and the hidden row's
+// Where the logits were kept: loss, normaliser and their gradient in place, and the hidden row's
 // copy for d_weight's product (zeros when ignored); one CTA per token.  Reads
 // 4 and writes 2 bytes a logit, which is what bounds it: 4096 x 163840, 4.0 GB,
 // take 631 us (6.4 TB/s).  In place, so that a block's logits need no second
@@ -174,19 +208,10 @@ __global__ void __launch_bounds__(kRowThreads, 3) ce_grad_rows_kernel(const __gr
     load(8 * threadIdx.x, x, y);
     const Row r = find_row<DT, kRowThreads>(b, t);
     if (threadIdx.x == 0) put_loss(b, t, r);
-    const TG* h = static_cast<const TG*>(b.hidden) + t * b.hidden_ld;
-    TG* copy = static_cast<TG*>(b.packed) + t * b.packed_ld;
-    if (wide_rows(b)) {
-        for (int64_t c = 8 * threadIdx.x; c < b.dim; c += 8 * kRowThreads)
-            *reinterpret_cast<uint4*>(copy + c) =
-                r.live ? *reinterpret_cast<const uint4*>(h + c) : make_uint4(0u, 0u, 0u, 0u);
-    } else {
-        for (int64_t c = threadIdx.x; c < b.dim; c += kRowThreads) copy[c] = r.live ? h[c] : Elem<DT>::store(0.f);
-    }
-    const float top = b.scalars[0];
-    const float scale = ce_grad_lift(DT) * (b.row_scale ? (top > 0.f ? b.row_scale[t] / top : 0.f) : 1.f);
+    copy_hidden<DT, kRowThreads>(b, t, r.live);
+    const float scale = grad_scale<DT>(b, t);
     const float c2 = b.logit_scale * kLog2e;
-    const float hot = exp2_fast(r.zt * kLog2e - r.lse2) - 1.f;
+    const float hot = hot_of(r);
     int sweep = 0;
     for (int64_t v0 = 0; v0 < b.vocab; v0 += kRowStep, ++sweep) {
         const int64_t v = v0 + 8 * threadIdx.x;

@@ -74,6 +74,14 @@ enum { GROUP_NONE = 0, GROUP_M = 1, GROUP_K = 2 };
 // Softmax sums of the product's rows, two pairs per row and column tile:
 // (top, sum over half the tile of exp2(x - top)), x = scale2 * product, without
 // the row's target column.  The product itself is stored when `store` is set.
+// What the logits' gradient needs of a row, see cross_entropy.cu.
+struct alignas(16) CeRow {
+    float lse2;   // normaliser, base 2
+    float scale;  // of the row's gradient
+    float hot;    // exp(z - lse) - 1 at the target
+    int32_t target;  // -1: the row is ignored
+};
+
 struct CeEpilogue {
     float2* sums;         // [M][column tile][half]; null: no softmax
     const void* targets;
@@ -84,6 +92,7 @@ struct CeEpilogue {
     const float* row_scale;  // the call's, may be null
     int64_t tokens;          // of the call
     int64_t ignore_index;
+    const CeRow* rows;       // not null: C becomes the logits' gradient
     float* scalars;          // [0] the largest |row_scale| of the tokens that count (1 when null), [1] that times factor
     float factor;
 };
@@ -138,6 +147,7 @@ struct CeBlock {
     float* loss;
     float* lse;
     float* Z;                // logits; turned in place into the gradient's 16-bit rows
+    CeRow* rows;             // null, or where launch_ce_finish writes them (and the packed copy)
     void* packed;            // copy of the hidden rows for d_weight, zeros for ignored tokens
     int* status;
     int64_t hidden_ld, weight_ld, packed_ld, z_ld;
@@ -145,7 +155,8 @@ struct CeBlock {
     int32_t targets64, dtype;
     float logit_scale;
 };
-// Loss and normaliser from the tiles' sums and the target's logit.
+// Loss and normaliser from the tiles' sums and the target's logit; with `rows`
+// also these and the packed copy.
 cudaError_t launch_ce_finish(const CeBlock& b, cudaStream_t st);
 // The same, the logits turned into their gradient, and the packed copy.
 cudaError_t launch_ce_grad_rows(const CeBlock& b, cudaStream_t st);

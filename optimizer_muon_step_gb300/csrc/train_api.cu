@@ -176,14 +176,24 @@ namespace {
 // 16-byte), the fp32 sums of d_weight (several blocks and a 16-bit result),
 // then for a block of tokens: the column tiles' softmax sums, the packed
 // hidden rows, and with gradients the rows
-// of logits and the pieces of d_hidden.
+// of logits (or of their gradient and what it needs of each row) and the pieces
+// of d_hidden.
 struct CeLayout {
     int64_t z_ld = 0, h_ld = 0, w_ld = 0, part_ld = 0;
     int splits = 1;      // pieces of the vocabulary in d_hidden's product
     int last_splits = 1; // and in that of a shorter last block
     bool pack_w = false, pack_h = false, sums = false;
-    size_t w_off = 0, sum_off = 0, tile_off = 0, h_off = 0, z_off = 0, part_off = 0, total = 0;
+    bool again = false;  // the logits are computed twice instead of kept
+    size_t w_off = 0, sum_off = 0, tile_off = 0, h_off = 0, z_off = 0, row_off = 0, part_off = 0, total = 0;
 };
+
+// Widths up to which a gradient computes the logits twice: once for their
+// sums, once to be turned into their gradient in the epilogue, which then
+// writes 2 bytes a logit where keeping them writes 4, reads 4 and writes 2.
+// Whole gradients, twice and kept: 3330 x 36344, K 128, 237 and 324 us; K 512,
+// 332 and 422; K 768, 458 and 515; K 1000, 741 and 689; 999 x 32003, K 256, 95
+// and 110; K 1024, 194 and 186; 16 x 50000, K 512, 62 and 65; K 1024, 98 and 93.
+constexpr int64_t kTwiceDim = 768;
 
 constexpr size_t kScalarsOff = 256;
 constexpr size_t kFixedBytes = 512;
@@ -238,7 +248,9 @@ size_t ce_total(const muon_linear_ce_t* p, bool grad, int64_t block, CeLayout* L
     L->sum_off = take(at, L->sums ? 4 * v * d : 0);
     L->tile_off = take(at, 8 * block * train_gemm_max_sums(v));
     L->h_off = take(at, grad || L->pack_h ? 2 * block * L->h_ld : 0);
-    L->z_off = take(at, grad ? 4 * block * L->z_ld : 0);
+    L->again = grad && d <= kTwiceDim;
+    L->z_off = take(at, grad ? (L->again ? 2 : 4) * block * L->z_ld : 0);
+    L->row_off = take(at, L->again ? static_cast<int64_t>(sizeof(CeRow)) * block : 0);
     L->part_off = take(at, 4 * pieces * L->part_ld);
     L->total = at;
     return at;
@@ -256,7 +268,7 @@ bool ce_sizes_ok(const muon_linear_ce_t* p) {
 // by one, from as many as have room for their logits and sums on.
 int64_t ce_block(const muon_linear_ce_t* p, bool grad, size_t bytes, CeLayout* L) {
     if (ce_total(p, grad, p->tokens, L) <= bytes) return p->tokens;
-    const int64_t row = 8 * train_gemm_max_sums(p->vocab) + (grad ? 4 * pitch64(p->vocab) : 0);
+    const int64_t row = 8 * train_gemm_max_sums(p->vocab) + (grad ? (p->dim <= kTwiceDim ? 2 : 4) * pitch64(p->vocab) : 0);
     for (int64_t n = std::min(p->tokens / 256, static_cast<int64_t>(bytes / 256) / row); n > 0; --n)
         if (ce_total(p, grad, 256 * n, L) <= bytes) return 256 * n;
     return 0;
@@ -331,6 +343,7 @@ muon_status_t ce_run(const muon_linear_ce_t* p, bool grad, void* workspace, size
         c.loss = p->loss + t0;
         c.lse = p->lse + t0;
         c.Z = reinterpret_cast<float*>(ws + L.z_off);
+        c.rows = L.again ? reinterpret_cast<CeRow*>(ws + L.row_off) : nullptr;
         c.z_ld = L.z_ld;
         c.packed = ws + L.h_off;
         c.packed_ld = L.h_ld;
@@ -350,7 +363,8 @@ muon_status_t ce_run(const muon_linear_ce_t* p, bool grad, void* workspace, size
         g.lda = L.pack_h ? L.h_ld : p->hidden_ld;
         g.B = weight;
         g.ldb = L.w_ld;
-        g.C = grad ? c.Z : nullptr;
+        const bool store = grad && !L.again;
+        g.C = store ? c.Z : nullptr;
         g.ldc = L.z_ld;
         g.c_dtype = MUON_F32;
         g.M = m;
@@ -362,7 +376,7 @@ muon_status_t ce_run(const muon_linear_ce_t* p, bool grad, void* workspace, size
         g.ce.sums = reinterpret_cast<float2*>(ws + L.tile_off);
         g.ce.targets = c.targets;
         g.ce.targets64 = c.targets64;
-        g.ce.store = grad;
+        g.ce.store = store;
         g.ce.first = t0 == 0;
         g.ce.scale2 = p->logit_scale * 1.4426950408889634f;
         g.ce.row_scale = grad ? p->row_scale : nullptr;
@@ -372,15 +386,25 @@ muon_status_t ce_run(const muon_linear_ce_t* p, bool grad, void* workspace, size
         g.ce.factor = p->logit_scale / ce_grad_lift(p->dtype);
         g.kind = MUON_KERNEL_CE_LOGITS;
         e = train_gemm(g, num_sms, st);
-        if (e == cudaSuccess) e = grad ? launch_ce_grad_rows(c, st) : launch_ce_finish(c, st);
+        if (e == cudaSuccess) e = store ? launch_ce_grad_rows(c, st) : launch_ce_finish(c, st);
+        if (e == cudaSuccess && L.again) {
+            g.C = c.Z;
+            g.c_dtype = p->dtype;
+            g.ce.sums = nullptr;
+            g.ce.first = 0;
+            g.ce.rows = c.rows;
+            g.kind = MUON_KERNEL_CE_GRAD;
+            e = train_gemm(g, num_sms, st);
+        }
         if (e != cudaSuccess || !grad) continue;
-        // d_hidden = G W; the rows of G lie in the front halves of Z's rows
+        // d_hidden = G W; kept logits leave G's rows in the front halves of theirs
+        const int64_t g_ld = L.again ? L.z_ld : 2 * L.z_ld;
         const int splits = m == block ? L.splits : L.last_splits;
         void* dh = static_cast<uint8_t*>(p->d_hidden) + 2 * t0 * d;
         float* parts = reinterpret_cast<float*>(ws + L.part_off);
         g = TrainGemm{};
         g.A = c.Z;
-        g.lda = 2 * L.z_ld;
+        g.lda = g_ld;
         g.B = weight;
         g.ldb = L.w_ld;
         g.b_mn = true;
@@ -406,7 +430,7 @@ muon_status_t ce_run(const muon_linear_ce_t* p, bool grad, void* workspace, size
         // d_weight += G^T H
         g = TrainGemm{};
         g.A = c.Z;
-        g.lda = 2 * L.z_ld;
+        g.lda = g_ld;
         g.a_mn = g.a_padded = true;
         g.B = c.packed;
         g.ldb = L.h_ld;

@@ -34,7 +34,9 @@
 //
 // The softmax epilogue (CE) reduces each row of a logits tile to its maximum
 // and sum of exponentials straight from TMEM; the logits are stored only
-// when their gradient is wanted.
+// when their gradient is wanted and the product is too wide to be repeated.
+// The repeated one ends in GRAD, which needs the normalisers that the first
+// one's sums gave.
 //
 // What bounds it, bf16, on a card that holds 1.3 to 1.5 GHz under this load:
 //   16 rows x 163840 columns, K 2048     reading the 671 MB of B: 109 us
@@ -78,7 +80,7 @@ constexpr int SMEM_BYTES = 1024 + RING_BYTES + EBUFS_BYTES + 1024;
 // count (2e-6 off at 2048, 9e-6 at 8192), 16384 (2e-5) where the result is
 // rounded to 16 bits.
 constexpr int kExactTerms = 1024, kRoundedTerms = 16384;
-enum { END_STORE = 0, END_CE = 1, END_TOKENS = 2, END_STORE_LONG = 3, END_CE_LONG = 4, ENDS = 5 };
+enum { END_STORE = 0, END_CE = 1, END_TOKENS = 2, END_STORE_LONG = 3, END_CE_LONG = 4, END_GRAD = 5, ENDS = 6 };
 
 struct GemmParams {
     CUtensorMap tm_a, tm_b, tm_c;
@@ -350,6 +352,12 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     return r;
 }
 
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -392,6 +400,19 @@ struct RowSums {
     }
 };
 
+// 64 logits of a row from column c on, turned into their gradient.
+__device__ __forceinline__ void logits_to_grad(float (&v)[64], const CeRow& r, float scale2, int c) {
+    const uint64_t s2 = pack2(scale2, scale2), l2 = pack2(-r.lse2, -r.lse2), f2 = pack2(r.scale, r.scale);
+    const int off = r.target - c;
+#pragma unroll
+    for (int k = 0; k < 64; k += 2) {
+        const float2 x = unpack2(fma2(pack2(v[k], v[k + 1]), s2, l2));
+        const float2 g = unpack2(mul2(pack2(k == off ? r.hot : ex2(x.x), k + 1 == off ? r.hot : ex2(x.y)), f2));
+        v[k] = r.target >= 0 ? g.x : 0.f;
+        v[k + 1] = r.target >= 0 ? g.y : 0.f;
+    }
+}
+
 // The scalars of a loss call, by one warp while the first tile's products
 // are under way.  Ignored tokens' scales do not count, whatever they hold.
 __device__ __forceinline__ void write_scalars(const CeEpilogue& ce, int64_t vocab, int lane) {
@@ -419,6 +440,7 @@ __device__ __forceinline__ void write_scalars(const CeEpilogue& ce, int64_t voca
 template <bool kPair, int kEnd>
 __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
     constexpr bool kCe = kEnd == END_CE || kEnd == END_CE_LONG;
+    constexpr bool kGrad = kEnd == END_GRAD;
     constexpr bool kLong = kEnd == END_CE_LONG || kEnd == END_STORE_LONG;
     constexpr int TILE_M = kPair ? 2 * BM : BM;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -735,7 +757,7 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
                 const int cols = min((half ? p.bn : mid) - lo, p.N - tile.col0 - lo);
                 // an empty group adds nothing
                 const bool mine = row < tile.rows_end && cols > 0 && (live || !p.accumulate);
-                const bool wide = p.c_dtype == MUON_F32;
+                const bool wide = !kGrad && p.c_dtype == MUON_F32;
 
                 RowSums rs = {-INFINITY, 0.f};
                 int target = -1;
@@ -743,6 +765,8 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
                     const int64_t tg = load_index(p.ce.targets, p.ce.targets64, row + lane);
                     target = tg >= 0 && tg < p.N ? static_cast<int>(tg) : -1;
                 }
+                CeRow ce_row = {0.f, 0.f, 0.f, -1};
+                if (kGrad && mine && row + lane < p.M) ce_row = p.ce.rows[row + lane];
                 // a finished block: out of shared memory to C at column c of this warp's
                 auto put = [&](int c) {
                     const int col = tile.col0 + lo + c;
@@ -866,7 +890,9 @@ __device__ __forceinline__ void train_gemm_body(const GemmParams& p) {
 #pragma unroll
                                 for (int k = 0; k < 64; ++k) v[k] = 0.f;
                             }
-                            if (alpha != 1.f) {
+                            if (kGrad) {
+                                logits_to_grad(v, ce_row, p.ce.scale2, tile.col0 + lo + c);
+                            } else if (alpha != 1.f) {
 #pragma unroll
                                 for (int k = 0; k < 64; ++k) v[k] *= alpha;
                             }
@@ -1050,13 +1076,14 @@ typedef void (*GemmKernel)(const GemmParams);
 
 GemmKernel single_kernel(int end) {
     static const GemmKernel k[ENDS] = {train_gemm_kernel<0>, train_gemm_kernel<1>, train_gemm_kernel<2>,
-                                       train_gemm_kernel<3>, train_gemm_kernel<4>};
+                                       train_gemm_kernel<3>, train_gemm_kernel<4>, train_gemm_kernel<5>};
     return k[end];
 }
 
 GemmKernel pair_kernel(int end) {
     static const GemmKernel k[ENDS] = {train_gemm_pair_kernel<0>, train_gemm_pair_kernel<1>, train_gemm_pair_kernel<2>,
-                                       train_gemm_pair_kernel<3>, train_gemm_pair_kernel<4>};
+                                       train_gemm_pair_kernel<3>, train_gemm_pair_kernel<4>,
+                                       train_gemm_pair_kernel<5>};
     return k[end];
 }
 
@@ -1159,6 +1186,7 @@ cudaError_t train_gemm(const TrainGemm& g, int num_sms, cudaStream_t st) {
                           : exact || g.K > 8 * limit ? g.K : 2 * g.K / g.groups;
     const bool longer = g.group != GROUP_M && terms > limit;
     const int end = g.group == GROUP_M ? END_TOKENS
+                    : g.ce.rows        ? END_GRAD
                     : g.ce.sums        ? (longer ? END_CE_LONG : END_CE)
                                        : (longer ? END_STORE_LONG : END_STORE);
     const int64_t a_count = g.group == GROUP_M ? g.groups : 1;

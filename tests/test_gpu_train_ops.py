@@ -332,6 +332,31 @@ def test_cross_entropy_in_blocks_of_tokens(lib, dtype):
     assert e.value.status == 4
 
 
+@pytest.mark.parametrize("d", [768, 776])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_cross_entropy_twice_and_kept(lib, dtype, d):
+    """Either side of the width up to which the logits are computed twice:
+    blocks of tokens, strided rows, ignored rows that hold NaN, scales."""
+    n, v = 700, 1100
+    hidden, weight, targets = ce_inputs(d, n, v, d, dtype, ignored=0.1)
+    targets[5], targets[600] = v, -3
+    out = (targets < 0) | (targets >= v)
+    scale = torch.rand(n, generator=gen(d), device=DEV) / n
+    want = ce_want(hidden, weight, targets, scale, 1.3, -100)
+    small = m.allocate_workspace(m.muon_linear_ce_workspace(hidden, weight, targets, True, budget_bytes=1))
+    held = torch.where(out, float("nan"), scale)
+    for pads, ws in (((0, 0), None), ((3, 5), None), ((8, 8), small)):
+        h = strided(torch.where(out[:, None], float("nan"), hidden.float()).to(dtype), pads[0])
+        got = m.muon_linear_ce_grad(h, strided(weight, pads[1]), targets, row_scale=held, logit_scale=1.3, workspace=ws)
+        live = ~out
+        within(got[0][live], want["loss"][live], want["loss_bound"][live], "loss")
+        within(got[1][live], want["lse"][live], want["lse_bound"][live], "lse")
+        assert (got[0][out] == 0).all() and (got[2][out] == 0).all()
+        within(got[2], want["dh"], rounded(want["bh"], want["dh"], dtype), "d_hidden")
+        bw = want["bw"] + 2.0 ** -22 * want["dw"].abs()
+        within(got[3], want["dw"], rounded(bw, want["dw"], dtype), "d_weight")
+
+
 def test_cross_entropy_short_last_block_stays_in_its_workspace(lib):
     """Blocks whose d_hidden is summed in one piece, then one in several."""
     n, v, d = 2048 + 44, 4096, 4864
