@@ -376,8 +376,13 @@ struct RowSums {
 #pragma unroll
         for (int k = 0; k < 32; k += 2) {
             const float2 x = unpack2(mul2(pack2(v[k], v[k + 1]), s2));
-            v[k] = (out >> k) & 1 ? -INFINITY : x.x;
-            v[k + 1] = (out >> (k + 1)) & 1 ? -INFINITY : x.y;
+            v[k] = x.x;
+            v[k + 1] = x.y;
+        }
+        if (__any_sync(0xffffffffu, out != 0)) {  // few blocks hold a target or the edge
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+                if ((out >> k) & 1) v[k] = -INFINITY;
         }
         float m[4] = {top, v[0], v[1], v[2]};
 #pragma unroll
