@@ -110,7 +110,10 @@ struct TrainGemm {
     int* status;
     CeEpilogue ce;
     int64_t groups;
-    int32_t splits;      // GROUP_NONE: pieces of K, piece s into C + s * c_stride
+    // Pieces of K.  GROUP_NONE: piece s into C + s * c_stride; GROUP_K: of every
+    // group's, piece s of group e into C + (s * groups + e) * c_stride.
+    int32_t splits;
+    bool exact;          // 32 bits of the pieces count
     int32_t offsets64;
     int32_t group;
     int32_t dtype;       // of A and B
@@ -126,10 +129,11 @@ size_t train_gemm_group_bytes(int64_t groups);
 int64_t train_gemm_sums(int64_t M, int64_t N, int64_t K);  // softmax sums per row: two per column tile
 int64_t train_gemm_max_sums(int64_t N);                    // whatever M and K are
 int64_t train_gemm_tiles(int64_t M, int64_t N);    // tiles of a plain product, one per CTA or CTA pair
-// out = alpha * the sum of `splits` fp32 matrices, in order.
+// out = alpha * the sum of `splits` fp32 matrices, in order; fp32 outputs may
+// be added to.
 cudaError_t launch_split_sum(const float* parts, int64_t ld, int64_t stride, int splits, float alpha,
                              const float* alpha_dev, void* out, int64_t out_ld, int out_dtype, int64_t rows,
-                             int64_t cols, int kind, int num_sms, cudaStream_t st);
+                             int64_t cols, bool accumulate, int kind, int num_sms, cudaStream_t st);
 
 // Copies rows of 2-byte elements to rows of another pitch.
 cudaError_t launch_pack(const void* src, int64_t src_ld, void* dst, int64_t dst_ld, int64_t rows, int64_t cols,

@@ -424,7 +424,7 @@ muon_status_t ce_run(const muon_linear_ce_t* p, bool grad, void* workspace, size
         g.kind = MUON_KERNEL_CE_GRAD;
         e = train_gemm(g, num_sms, st);
         if (e == cudaSuccess && splits > 1)
-            e = launch_split_sum(parts, L.part_ld, g.c_stride, splits, 1.f, scalars + 1, dh, d, p->dtype, m, d,
+            e = launch_split_sum(parts, L.part_ld, g.c_stride, splits, 1.f, scalars + 1, dh, d, p->dtype, m, d, false,
                                  MUON_KERNEL_CE_GRAD, num_sms, st);
         if (e != cudaSuccess) break;
         // d_weight += G^T H
@@ -487,6 +487,40 @@ namespace {
 bool expert_sizes_ok(int64_t experts, int64_t tokens, int64_t rows, int64_t cols) {
     return experts > 0 && experts <= 65536 && tokens >= 0 && tokens < kMaxExtent && rows > 0 && rows < kMaxExtent &&
            cols > 0 && cols < kMaxExtent && experts * rows < (int64_t(1) << 31) * 8;
+}
+
+// Pieces that every expert's tokens are cut into in the weight gradient, which
+// has few and long tiles when small matrices of few experts see many tokens.
+// The shares are on the device: half of the experts are taken to have all
+// tokens.  Cost as in hidden_splits; pieces must promise a fifth, as they cost
+// more where the shares are equal.  In pieces and in one: 4 experts, one with
+// all of 29007 tokens, 1936 -> 200, 54 and 145 us, with equal shares 43 and 44;
+// one expert, 32768 tokens, 1024 -> 1024, 52 and 145; 2 experts, 20100 tokens,
+// 128 -> 128, 16 and 84.  8 equal experts of 2000 tokens, 512 -> 512, which
+// stay in one, take 17 us, in two pieces 22.
+int wgrad_splits(int64_t experts, int64_t tokens, int64_t rows, int64_t cols) {
+    const int64_t tiles = train_gemm_tiles(rows, cols), workers = rows > 128 ? kSms / 2 : kSms;
+    if (experts * tiles > workers) return 1;
+    const int64_t busy = (experts + 1) / 2;
+    const double blocks = static_cast<double>((tokens + 63) / 64) / busy;
+    int best = 1;
+    double best_cost = 0;
+    for (int s = 1; s <= 16; ++s) {
+        const double waves = static_cast<double>((busy * tiles * s + workers - 1) / workers);
+        const double pieces = s > 1 ? 8.0 * s * experts * rows * cols / 5e12 / 0.35e-6 + 8 : 0;
+        const double cost = waves * (blocks / s + 10) + pieces;
+        if (s == 1 || cost < best_cost) {
+            best = s;
+            best_cost = s == 1 ? 0.8 * cost : cost;
+        }
+    }
+    return best;
+}
+
+// Bytes of those pieces, fp32 rows padded to 16 bytes.
+int64_t wgrad_part_bytes(int64_t experts, int64_t tokens, int64_t rows, int64_t cols) {
+    const int64_t s = wgrad_splits(experts, tokens, rows, cols);
+    return s > 1 ? round_up(4 * s * experts * rows * round_up(cols, 4), 256) : 0;
 }
 
 }  // namespace
@@ -575,7 +609,8 @@ size_t muon_expert_wgrad_workspace(const void* grad, int64_t grad_ld, const void
     size_t n = kHeaderBytes;
     if (!tma_ready(grad, grad_ld)) n += packed_bytes(tokens, rows);
     if (!tma_ready(x, x_ld)) n += packed_bytes(tokens, cols);
-    return n + static_cast<size_t>(round_up(static_cast<int64_t>(train_gemm_group_bytes(experts)), 256));
+    return n + static_cast<size_t>(round_up(static_cast<int64_t>(train_gemm_group_bytes(experts)), 256) +
+                                   wgrad_part_bytes(experts, tokens, rows, cols));
 }
 
 muon_status_t muon_expert_wgrad(const void* grad, int64_t grad_ld, const void* x, int64_t x_ld, const void* offsets,
@@ -617,6 +652,9 @@ muon_status_t muon_expert_wgrad(const void* grad, int64_t grad_ld, const void* x
     TrainGemm g = {};
     g.group_maps = at;
     at += round_up(static_cast<int64_t>(train_gemm_group_bytes(experts)), 256);
+    const int splits = wgrad_splits(experts, tokens, rows, cols);
+    float* parts = reinterpret_cast<float*>(at);
+    at += wgrad_part_bytes(experts, tokens, rows, cols);
     g.A = grad;
     g.lda = grad_ld;
     g.B = x;
@@ -635,11 +673,14 @@ muon_status_t muon_expert_wgrad(const void* grad, int64_t grad_ld, const void* x
     }
     if (e != cudaSuccess) return from_cuda(e);
     g.a_mn = g.b_mn = true;
-    g.C = d_weight;
-    g.ldc = cols;
-    g.c_stride = rows * cols;
-    g.c_dtype = d_weight_dtype;
-    g.accumulate = accumulate;
+    const int64_t part_ld = round_up(cols, 4);
+    g.C = splits > 1 ? parts : d_weight;
+    g.ldc = splits > 1 ? part_ld : cols;
+    g.c_stride = rows * g.ldc;
+    g.c_dtype = splits > 1 ? static_cast<int32_t>(MUON_F32) : d_weight_dtype;
+    g.accumulate = splits > 1 ? 0 : accumulate;
+    g.splits = splits;
+    g.exact = d_weight_dtype == MUON_F32;
     g.M = rows;
     g.N = cols;
     g.K = tokens;
@@ -651,7 +692,11 @@ muon_status_t muon_expert_wgrad(const void* grad, int64_t grad_ld, const void* x
     g.dtype = dtype;
     g.status = reinterpret_cast<int*>(ws);
     g.kind = MUON_KERNEL_EXPERT;
-    return from_cuda(train_gemm(g, num_sms, st));
+    e = train_gemm(g, num_sms, st);
+    if (e == cudaSuccess && splits > 1)
+        e = launch_split_sum(parts, part_ld, experts * rows * part_ld, splits, 1.f, nullptr, d_weight, cols,
+                             d_weight_dtype, experts * rows, cols, accumulate != 0, MUON_KERNEL_EXPERT, num_sms, st);
+    return from_cuda(e);
 }
 
 }  // extern "C"

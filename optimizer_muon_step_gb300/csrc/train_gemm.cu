@@ -4,7 +4,7 @@
 //
 //   GROUP_NONE  C = A B, K optionally split into pieces of their own output
 //   GROUP_M     rows [o_e, o_{e+1}) of A and C use B_e
-//   GROUP_K     C_e = sum over k in [o_e, o_{e+1})
+//   GROUP_K     C_e = sum over k in [o_e, o_{e+1}), each optionally split alike
 //
 // One persistent kernel of 11 warps per CTA (or CTA pair), with the roles of
 // the Newton-Schulz kernel: warp 0 feeds a shared-memory ring by TMA, warp 1
@@ -101,6 +101,7 @@ struct GemmParams {
     int32_t band;                   // rows of tiles walked together (GROUP_NONE, GROUP_K)
     int32_t groups, group, offsets64;
     int32_t k_blocks;               // per split (GROUP_NONE)
+    int32_t splits;                 // of every group (GROUP_K)
     int32_t c_dtype, accumulate, tma_c;
     int32_t chunked_a, chunked_b;   // MN-major maps are 4-D, two or four 64-row chunks a copy
     uint32_t idesc;                 // without M and N
@@ -166,9 +167,12 @@ struct Walker {
         if (p.group != GROUP_M) {
             if (t >= p.total_tiles) return false;
             const int per = p.tiles_m * p.tiles_n;
-            int s = t / per;
+            int s = t / per, piece = 0;
             const int r = t - s * per;
-            if (p.group == GROUP_K) s = p.order[s];
+            if (p.group == GROUP_K) {
+                piece = s % p.splits;
+                s = p.order[s / p.splits];
+            }
             const int span = p.band * p.tiles_n;
             const int b = r / span;
             const int rr = r - b * span;
@@ -185,11 +189,15 @@ struct Walker {
             const int rem = p.N - o.col0;
             const int q = TILE_M == BM ? 15 : p.b_mn && p.chunked_b ? 127 : 31;
             o.n = rem < p.bn ? (rem + q) & ~q : p.bn;
-            o.c2 = o.group = s;
+            o.group = s;
+            o.c2 = piece * p.groups + s;
             if (p.group == GROUP_K) {
                 const int a = clamped(p, s, p.K), e = clamped(p, s + 1, p.K);
-                o.k0 = a;
-                o.nk = e > a ? (e - a + BK - 1) / BK : 0;
+                const int all = e > a ? (e - a + BK - 1) / BK : 0;
+                const int per_piece = (all + p.splits - 1) / p.splits;
+                const int left_k = all - piece * per_piece;  // the last pieces may be empty
+                o.k0 = a + piece * per_piece * BK;
+                o.nk = left_k <= 0 ? 0 : left_k < per_piece ? left_k : per_piece;
             } else {
                 const int all = (p.K + BK - 1) / BK;
                 const int kb = s * p.k_blocks;
@@ -996,13 +1004,13 @@ __global__ void pack_kernel(const uint16_t* src, int64_t src_ld, uint16_t* dst, 
         for (int64_t c = threadIdx.x; c < cols; c += blockDim.x) dst[r * dst_ld + c] = src[r * src_ld + c];
 }
 
-// out = alpha * sum over the splits, in order; four columns a thread (rows
+// out = alpha * sum over the splits (+ out), in order; four columns a thread (rows
 // are padded to four).  The pieces come out of L2: 8 us for 999 x 1000 in 8
 // pieces, most of it the launch and the loads' latency.
 template <int DT>
 __global__ void __launch_bounds__(256) split_sum_kernel(const float* parts, int64_t ld, int64_t stride, int splits,
                                                         float alpha, const float* alpha_dev, void* out, int64_t out_ld,
-                                                        int64_t rows, int64_t cols) {
+                                                        int64_t rows, int64_t cols, bool accumulate) {
     pdl_wait_then_release();
     const float f = alpha_dev ? alpha * *alpha_dev : alpha;
     const int64_t quads = ld / 4, n = rows * quads;
@@ -1019,7 +1027,7 @@ __global__ void __launch_bounds__(256) split_sum_kernel(const float* parts, int6
         const float v[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            if (c + k < cols) o[k] = Elem<DT>::store(f * v[k]);
+            if (c + k < cols) o[k] = Elem<DT>::store(DT == MUON_F32 && accumulate ? Elem<DT>::load(o[k]) + f * v[k] : f * v[k]);
     }
 }
 
@@ -1180,15 +1188,16 @@ cudaError_t train_gemm(const TrainGemm& g, int num_sms, cudaStream_t st) {
     const bool pair = use_pairs(g);
     GemmParams p;
     memset(&p, 0, sizeof p);
-    const bool exact = g.ce.sums || (g.c_dtype == MUON_F32 && g.splits <= 1);
+    const bool exact = g.exact || g.ce.sums || (g.c_dtype == MUON_F32 && g.splits <= 1);
+    const int64_t pieces = g.splits > 1 ? g.splits : 1;
     // A group's share of K is not known here.  It may be all of it, which is
     // what is assumed where 32 bits count (64 experts of 32768 tokens, 2048 x
     // 1408, fp32 gradients: 200 us for 191); results of 16 bits assume twice
     // the average (150 us for 165) while the worst case, 1e-4 at eight times
     // the terms, stays below their rounding.  GROUP_M's K is a weight's width.
     const int64_t limit = exact ? kExactTerms : kRoundedTerms;
-    const int64_t terms = g.group != GROUP_K ? (g.splits > 1 ? g.K / g.splits : g.K)
-                          : exact || g.K > 8 * limit ? g.K : 2 * g.K / g.groups;
+    const int64_t most = g.K / pieces;
+    const int64_t terms = g.group != GROUP_K || exact || most > 8 * limit ? most : 2 * most / g.groups;
     const bool longer = g.group != GROUP_M && terms > limit;
     const int end = g.group == GROUP_M ? END_TOKENS
                     : g.ce.rows        ? END_GRAD
@@ -1232,7 +1241,7 @@ cudaError_t train_gemm(const TrainGemm& g, int num_sms, cudaStream_t st) {
     if (!g.b_mn) ok &= map3(&p.tm_b, g.B, g.dtype, g.K, g.N, 1, g.ldb, 0, static_cast<uint32_t>(pair ? bn / 2 : bn));
     else if (p.chunked_b) ok &= map_chunked(&p.tm_b, g.B, g.dtype, wb, g.K, 1, g.ldb, 0);
     else ok &= map3(&p.tm_b, g.B, g.dtype, g.N, g.K, 1, g.ldb, 0, BK);
-    const int64_t c_count = g.group == GROUP_K ? g.groups : g.splits > 1 ? g.splits : 1;
+    const int64_t c_count = g.group == GROUP_K ? pieces * g.groups : pieces;
     const int64_t ce = static_cast<int64_t>(dtype_bytes(g.c_dtype));
     p.tma_c = g.C && (reinterpret_cast<uintptr_t>(g.C) & 15) == 0 && g.ldc * ce % 16 == 0 &&
               (c_count <= 1 || g.c_stride * ce % 16 == 0);
@@ -1268,11 +1277,11 @@ cudaError_t train_gemm(const TrainGemm& g, int num_sms, cudaStream_t st) {
     if (g.group == GROUP_M) {
         tiles += (g.groups + 2) * static_cast<int64_t>(p.tiles_m);  // a bound: each group may end inside a tile
     } else if (g.group == GROUP_K) {
-        tiles *= g.groups;
+        p.splits = static_cast<int32_t>(pieces);
+        tiles *= pieces * g.groups;
     } else {
-        const int64_t splits = g.splits > 1 ? g.splits : 1;
-        p.k_blocks = static_cast<int32_t>((kb + splits - 1) / splits);
-        tiles *= splits;
+        p.k_blocks = static_cast<int32_t>((kb + pieces - 1) / pieces);
+        tiles *= pieces;
     }
     if (tiles > INT32_MAX) return cudaErrorInvalidValue;
     p.total_tiles = static_cast<int32_t>(tiles);
@@ -1317,13 +1326,15 @@ cudaError_t train_gemm(const TrainGemm& g, int num_sms, cudaStream_t st) {
 
 cudaError_t launch_split_sum(const float* parts, int64_t ld, int64_t stride, int splits, float alpha,
                              const float* alpha_dev, void* out, int64_t out_ld, int out_dtype, int64_t rows,
-                             int64_t cols, int kind, int num_sms, cudaStream_t st) {
+                             int64_t cols, bool accumulate, int kind, int num_sms, cudaStream_t st) {
     const int64_t blocks = (rows * (ld / 4) + 255) / 256;
     const dim3 grid(static_cast<unsigned>(blocks < num_sms * 8 ? blocks : num_sms * 8));
     launch_begin(kind, st);
-    const cudaError_t e =
-        launch_pdl(out_dtype == MUON_BF16 ? split_sum_kernel<MUON_BF16> : split_sum_kernel<MUON_F16>, grid, dim3(256), 0,
-                   st, parts, ld, stride, splits, alpha, alpha_dev, out, out_ld, rows, cols);
+    const cudaError_t e = launch_pdl(out_dtype == MUON_BF16  ? split_sum_kernel<MUON_BF16>
+                                     : out_dtype == MUON_F16 ? split_sum_kernel<MUON_F16>
+                                                             : split_sum_kernel<MUON_F32>,
+                                     grid, dim3(256), 0, st, parts, ld, stride, splits, alpha, alpha_dev, out, out_ld,
+                                     rows, cols, accumulate);
     launch_end(kind, st);
     return e;
 }

@@ -290,6 +290,39 @@ def test_expert_wgrad_long_sums(lib):
         expert_check(x, dy, w, off, BF)
 
 
+@pytest.mark.parametrize("sizes,rows,cols", [([0, 5000, 0], 200, 130), ([1, 9000], 96, 64), ([3000, 0, 64, 4097], 264, 257),
+                                             ([20000], 72, 1000)])
+def test_expert_wgrad_in_pieces(lib, sizes, rows, cols):
+    """Few and small matrices of many tokens: every expert's tokens are cut
+    into pieces whose sums are added."""
+    g = gen(rows)
+    n = sum(sizes)
+    off = torch.tensor([0, *torch.tensor(sizes).cumsum(0).tolist()], dtype=torch.int64, device=DEV)
+    one = m.load_library().muon_expert_wgrad_workspace(4096, 1024, 4096, 1024, len(sizes), 64, rows, cols)
+    assert m.load_library().muon_expert_wgrad_workspace(4096, 1024, 4096, 1024, len(sizes), n, rows, cols) > one
+    for dtype in (BF, HF):
+        x, dy = randn(g, (n, cols), 1.0, dtype), randn(g, (n, rows), 1.0, dtype)
+        start = torch.randn(len(sizes), rows, cols, generator=g, device=DEV)
+        want = torch.zeros(len(sizes), rows, cols, dtype=torch.float64, device=DEV)
+        mag = torch.zeros_like(want)
+        at = 0
+        for e, k in enumerate(sizes):
+            a, b = dy[at:at + k].double(), x[at:at + k].double()
+            want[e], mag[e] = a.t() @ b, a.abs().t() @ b.abs()
+            at += k
+        bound = mma_bound(max(sizes), mag)
+        got = m.muon_expert_wgrad(dy, x, off)
+        within(got, want, rounded(bound, want, dtype), "rounded")
+        assert torch.equal(got, m.muon_expert_wgrad(dy, x, off))
+        within(m.muon_expert_wgrad(dy, x, off, out_dtype=F32), want, bound, "fp32")
+        acc = start.clone()
+        m.muon_expert_wgrad(dy, x, off, out=acc, accumulate=True)
+        total = want + start.double()
+        within(acc, total, bound + 2.0 ** -22 * (total.abs() + start.double().abs() + bound), "accumulated")
+    for e, k in enumerate(sizes):
+        assert k > 0 or (got[e] == 0).all()
+
+
 def test_expert_wgrad_one_long_sum_of_many(lib):
     """One expert has all of 20000 tokens: its fp32 sums of positive products
     are cut too.  A segment's 1024 terms are 64 tensor-core additions, off by
