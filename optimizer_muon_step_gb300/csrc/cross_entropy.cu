@@ -9,7 +9,8 @@
 // cores, and the tiles' sums leave its column out: a trained model's loss is
 // the difference of a normaliser that the target's logit dominates and that
 // same logit, and the tensor core's accumulator truncates (2e-6 of the result
-// at 2048 terms against 4e-7 for fp32 sums).
+// at 2048 terms against 4e-7 for fp32 sums).  Where it is the largest, the loss
+// is ln(1 + sum over the others exp(z_v - z_target)).
 #include <math.h>
 
 #include "train.h"
@@ -43,7 +44,7 @@ __device__ __forceinline__ float2 join(float2 a, float2 b) {
 struct Row {
     int64_t target;
     bool inside, live;
-    float zt, lse2;
+    float zt, loss, lse, lse2;
 };
 
 // 16-byte rows on both sides?
@@ -109,8 +110,18 @@ __device__ __forceinline__ Row find_row(const CeBlock& b, int64_t t) {
     for (int i = 1; i < kWarps; ++i) sum += sums[i];
     acc = make_float2(top, sum);
     r.zt = b.logit_scale * s;
-    if (r.inside) acc = join(acc, make_float2(r.zt * kLog2e, isnan(r.zt) ? r.zt : 1.f));
-    r.lse2 = (isinf(acc.x) ? 0.f : acc.x) + log2f(acc.y);
+    const float zt2 = r.zt * kLog2e;
+    if (r.inside && zt2 >= acc.x && !isinf(zt2)) {
+        // the target has the largest logit: small losses keep all their bits
+        r.loss = log1pf(rescaled(acc, zt2));
+        r.lse = r.zt + r.loss;
+        r.lse2 = fmaf(r.loss, kLog2e, zt2);
+    } else {
+        if (r.inside) acc = join(acc, make_float2(zt2, isnan(zt2) ? zt2 : 1.f));
+        r.lse2 = (isinf(acc.x) ? 0.f : acc.x) + log2f(acc.y);
+        r.lse = r.lse2 * kLn2;
+        r.loss = r.lse - r.zt;
+    }
     return r;
 }
 
@@ -138,9 +149,8 @@ __device__ __forceinline__ void copy_hidden(const CeBlock& b, int64_t t, bool li
 }
 
 __device__ __forceinline__ void put_loss(const CeBlock& b, int64_t t, const Row& r) {
-    const float lse = r.lse2 * kLn2;
-    b.lse[t] = lse;
-    b.loss[t] = r.live ? lse - r.zt : 0.f;
+    b.lse[t] = r.lse;
+    b.loss[t] = r.live ? r.loss : 0.f;
     if (!r.inside && r.target != b.ignore_index) atomicCAS(b.status, 0, static_cast<int>(MUON_ERR_INVALID_ARG));
 }
 

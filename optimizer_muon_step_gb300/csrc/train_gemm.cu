@@ -76,10 +76,11 @@ constexpr int SMEM_BYTES = 1024 + RING_BYTES + EBUFS_BYTES + 1024;
 // What a product's tiles end in.
 // The LONG ones cut the sum over K into segments (see the epilogue); they
 // take 1 to 3% longer in the loss, 4 to 10% in GROUP_K's short sums.
-// Terms summed by the tensor core in one go: 1024 where 32 bits of the sum
-// count (2e-6 off at 2048, 9e-6 at 8192), 16384 (2e-5) where the result is
-// rounded to 16 bits.
-constexpr int kExactTerms = 1024, kRoundedTerms = 16384;
+// Terms summed by the tensor core in one go: 512 where 32 bits of the sum
+// count (2e-6 off at 656 where they have one sign; 999 x 32003, K 1000: 206 us
+// the whole gradient, in one go 200, by 256 219), 16384 (2e-5) where the result
+// is rounded to 16 bits.
+constexpr int kExactTerms = 512, kRoundedTerms = 16384;
 enum { END_STORE = 0, END_CE = 1, END_TOKENS = 2, END_STORE_LONG = 3, END_CE_LONG = 4, END_GRAD = 5, ENDS = 6 };
 
 struct GemmParams {

@@ -262,6 +262,26 @@ def test_cross_entropy_loss_of_many_tokens(lib, dtype):
     within(lse, want["lse"], want["lse_bound"], "lse")
 
 
+@pytest.mark.parametrize("n,v,d", [(5, 300, 64), (200, 3000, 520), (40, 900, 1100)])
+def test_cross_entropy_small_losses_keep_their_bits(lib, n, v, d):
+    """The target's logit leads by 10 and more: losses of 1e-3 and less are sums of
+    small terms, not differences of large ones.  A loss is off by a factor of
+    1 + 2 dz (the error of two logits) + 2^-18 (exponentials and their
+    arguments) + v 2^-24 (the sum) at most, with dz from fp32 and tensor-core
+    sums of d products."""
+    g = gen(v)
+    weight = randn(g, (v, d), 0.5 / math.sqrt(d), BF)
+    targets = torch.randint(0, v, (n,), generator=g, device=DEV)
+    hidden = (weight[targets].float() * 80).to(BF)
+    z = hidden.double() @ weight.double().t()
+    zt = z.gather(1, targets[:, None])
+    want = torch.log1p(torch.exp(z - zt).sum(1) - 1)
+    dz = mma_bound(d, hidden.double().abs() @ weight.double().abs().t()).max(dim=1).values + 2.0 ** -22 * z.abs().max(1).values
+    loss, lse = m.muon_linear_ce(hidden, weight, targets)
+    assert want.max() < 0.1
+    within(loss, want, want * (torch.expm1(2 * dz) + 2.0 ** -18 + v * 2.0 ** -24), "loss")
+
+
 @pytest.mark.parametrize("n,v,d", [(100, 900, 1400), (200, 1500, 2056), (1100, 100, 72), (1100, 400, 72), (1800, 20000, 2048),
                                    (128, 100000, 7168)])
 def test_cross_entropy_long_sums(lib, n, v, d):
