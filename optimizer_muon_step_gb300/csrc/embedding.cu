@@ -419,6 +419,19 @@ __device__ __forceinline__ void put_row(float* row, int64_t c0, int64_t dim, int
     }
 }
 
+template <int DT>
+__device__ __forceinline__ uint32_t load_bits(const typename Elem<DT>::T* p) {
+    if constexpr (DT == MUON_F32) return *reinterpret_cast<const uint32_t*>(p);
+    else return *reinterpret_cast<const uint16_t*>(p);
+}
+
+template <int DT>
+__device__ __forceinline__ float bits_to_float(uint32_t w) {
+    if constexpr (DT == MUON_F32) return __uint_as_float(w);
+    else if constexpr (DT == MUON_BF16) return __uint_as_float(w << 16);
+    else return __half2float(__ushort_as_half(static_cast<unsigned short>(w)));
+}
+
 template <int GD, bool kWide>
 __device__ __forceinline__ void sum_piece(const SumArgs& a, int piece, int64_t c0, int lane) {
     typedef typename Elem<GD>::T TG;
@@ -438,9 +451,13 @@ __device__ __forceinline__ void sum_piece(const SumArgs& a, int piece, int64_t c
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.f;
     bool began = __shfl_sync(0xffffffffu, key, 0) != prev;  // the current run's first token is in this piece
-    constexpr int kBatch = kWide && GD == MUON_F32 ? 4 : 8;  // tokens loaded together
+    constexpr int kBatch = kWide && GD != MUON_F32 ? 8 : 4;  // tokens loaded together
     for (int j0 = 0; j0 < n; j0 += kBatch) {
-        typename std::conditional<kWide, Raw8<GD>, float[8]>::type v[kBatch];
+        // Single elements are kept as they lie in memory, one to a register, and
+        // loaded without conditions (from column or token 0 where there is
+        // none): conditional ones wait for each other (5899 tokens of 5266 bf16:
+        // 158 us for the whole gradient, 64 so).
+        typename std::conditional<kWide, Raw8<GD>, uint32_t[8]>::type v[kBatch];
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
             const int64_t t = __shfl_sync(0xffffffffu, pos, (j0 + j) & 31);
@@ -449,13 +466,9 @@ __device__ __forceinline__ void sum_piece(const SumArgs& a, int piece, int64_t c
                 if (j0 + j < n && c0 + lane * 8 < a.dim) v[j] = load_raw8<GD>(src + c0 + lane * 8);
             } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[j][i] = 0.f;
-                if (j0 + j < n) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int64_t c = column<false>(c0, lane, i);
-                        if (c < a.dim) v[j][i] = Elem<GD>::load(src[c]);
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    const int64_t c = column<false>(c0, lane, i);
+                    v[j][i] = load_bits<GD>(src + (c < a.dim ? c : 0));
                 }
             }
         }
@@ -470,7 +483,7 @@ __device__ __forceinline__ void sum_piece(const SumArgs& a, int piece, int64_t c
                     for (int i = 0; i < 8; ++i) acc[i] += f[i];
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) acc[i] += v[j][i];
+                    for (int i = 0; i < 8; ++i) acc[i] += bits_to_float<GD>(v[j][i]);
                 }
                 const int k = __shfl_sync(0xffffffffu, key, l);
                 const int after = l + 1 < n ? __shfl_sync(0xffffffffu, key, (l + 1) & 31) : next;
@@ -497,7 +510,7 @@ __device__ __forceinline__ void sum_piece(const SumArgs& a, int piece, int64_t c
 }
 
 template <int GD, bool kWide>
-__global__ void __launch_bounds__(32 * kSumWarps, kWide ? 6 : 4) embed_sum_kernel(const __grid_constant__ SumArgs a) {
+__global__ void __launch_bounds__(32 * kSumWarps, kWide ? 5 : 4) embed_sum_kernel(const __grid_constant__ SumArgs a) {
     pdl_wait_then_release();
     const int64_t task = blockIdx.x * int64_t(kSumWarps) + (threadIdx.x >> 5);
     const int64_t piece = task / a.col_tasks;
