@@ -96,9 +96,24 @@ __device__ __forceinline__ void store8(typename Elem<DT>::T* p, const float (&v)
     }
 }
 
-// kWide: every row of both matrices starts on 16 bytes and has a multiple of
-// 8 elements; otherwise the warp moves single elements, side by side.
-template <int TD, int OD, bool kWide>
+template <int DT>
+__device__ __forceinline__ uint32_t load_bits(const typename Elem<DT>::T* p) {
+    if constexpr (DT == MUON_F32) return *reinterpret_cast<const uint32_t*>(p);
+    else return *reinterpret_cast<const uint16_t*>(p);
+}
+
+template <int DT>
+__device__ __forceinline__ float bits_to_float(uint32_t w) {
+    if constexpr (DT == MUON_F32) return __uint_as_float(w);
+    else if constexpr (DT == MUON_BF16) return __uint_as_float(w << 16);
+    else return __half2float(__ushort_as_half(static_cast<unsigned short>(w)));
+}
+
+// ROWS_WIDE: every row of both matrices starts on 16 bytes and has a multiple
+// of 8 elements; otherwise the warp moves single elements, side by side.
+enum { ROWS_WIDE, ROWS_LONG, ROWS_SHORT };
+constexpr int64_t kLongRow = 768;
+template <int TD, int OD, int kRows>
 __global__ void __launch_bounds__(256) embed_lookup_kernel(const __grid_constant__ EmbedLookup a, int segs) {
     typedef typename Elem<TD>::T TI;
     typedef typename Elem<OD>::T TO;
@@ -111,7 +126,7 @@ __global__ void __launch_bounds__(256) embed_lookup_kernel(const __grid_constant
     const bool live = id >= 0 && id < a.vocab && id != a.padding_idx;
     const TI* src = static_cast<const TI*>(a.table) + (live ? id : 0) * a.table_ld;
     TO* dst = static_cast<TO*>(a.out) + t * a.out_ld;
-    if constexpr (kWide) {
+    if constexpr (kRows == ROWS_WIDE) {
         float v[kUnroll][8];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
@@ -129,9 +144,27 @@ __global__ void __launch_bounds__(256) embed_lookup_kernel(const __grid_constant
         }
     } else {
         const int64_t end = c0 + kSeg < a.dim ? c0 + kSeg : a.dim;
+        if constexpr (kRows == ROWS_LONG) {
+            // Loads first, from column 0 where there is none: a load after a store,
+            // or one under a condition, waits (20395 tokens of 7001, fp32 to bf16:
+            // 131 us, 281 as below).
+            constexpr int kTogether = 16;
+            for (int64_t c1 = c0 + lane; c1 < end; c1 += 32 * kTogether) {
+                uint32_t v[kTogether];
+#pragma unroll
+                for (int i = 0; i < kTogether; ++i) v[i] = load_bits<TD>(src + (c1 + 32 * i < end ? c1 + 32 * i : 0));
+#pragma unroll
+                for (int i = 0; i < kTogether; ++i)
+                    if (c1 + 32 * i < end)
+                        dst[c1 + 32 * i] = Elem<OD>::store(live ? a.scale * bits_to_float<TD>(v[i]) : 0.f);
+            }
+        } else {
+            // short rows have too few columns for that, and want more warps (30000
+            // tokens of 514, bf16: 19 us, 27 as above)
 #pragma unroll 8
-        for (int64_t c = c0 + lane; c < end; c += 32)
-            dst[c] = Elem<OD>::store(live ? a.scale * Elem<TD>::load(src[c]) : 0.f);
+            for (int64_t c = c0 + lane; c < end; c += 32)
+                dst[c] = Elem<OD>::store(live ? a.scale * Elem<TD>::load(src[c]) : 0.f);
+        }
     }
 }
 
@@ -142,8 +175,9 @@ void lookup_go(const EmbedLookup& a, cudaStream_t st) {
                       (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && a.out_ld * oe % 16 == 0;
     const int segs = static_cast<int>((a.dim + kSeg - 1) / kSeg);
     const unsigned grid = static_cast<unsigned>((a.tokens * segs + 7) / 8);
-    if (wide) embed_lookup_kernel<TD, OD, true><<<grid, 256, 0, st>>>(a, segs);
-    else embed_lookup_kernel<TD, OD, false><<<grid, 256, 0, st>>>(a, segs);
+    if (wide) embed_lookup_kernel<TD, OD, ROWS_WIDE><<<grid, 256, 0, st>>>(a, segs);
+    else if (a.dim > kLongRow) embed_lookup_kernel<TD, OD, ROWS_LONG><<<grid, 256, 0, st>>>(a, segs);
+    else embed_lookup_kernel<TD, OD, ROWS_SHORT><<<grid, 256, 0, st>>>(a, segs);
 }
 
 template <int TD>
@@ -417,19 +451,6 @@ __device__ __forceinline__ void put_row(float* row, int64_t c0, int64_t dim, int
             if (c < dim) row[c] = accumulate ? row[c] + scale * v[i] : scale * v[i];
         }
     }
-}
-
-template <int DT>
-__device__ __forceinline__ uint32_t load_bits(const typename Elem<DT>::T* p) {
-    if constexpr (DT == MUON_F32) return *reinterpret_cast<const uint32_t*>(p);
-    else return *reinterpret_cast<const uint16_t*>(p);
-}
-
-template <int DT>
-__device__ __forceinline__ float bits_to_float(uint32_t w) {
-    if constexpr (DT == MUON_F32) return __uint_as_float(w);
-    else if constexpr (DT == MUON_BF16) return __uint_as_float(w << 16);
-    else return __half2float(__ushort_as_half(static_cast<unsigned short>(w)));
 }
 
 template <int GD, bool kWide>
